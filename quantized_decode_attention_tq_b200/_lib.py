@@ -15,6 +15,9 @@ TQ_DEV_POS_RANGE, TQ_DEV_NORM_OVERFLOW, TQ_DEV_LEN_RANGE, TQ_DEV_INTERNAL, TQ_DE
 TQ_MAX_OUTLIERS = 16
 TQ_F32, TQ_F16 = 0, 1
 TQ_MAX_QUERY_TOKENS = 16
+TQ_BF16 = 2  # include/tq_spec.h only
+TQ_MAX_TREE_NODES = 64
+TQ_MAX_ROT_DIM = 512
 
 # Every symbol include/tq.h declares, with (restype, argtypes).
 c_int, c_float, c_size_t, c_void_p = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
@@ -35,6 +38,21 @@ class KVDesc(ctypes.Structure):
 
 class VOutliers(ctypes.Structure):
     _fields_ = [("k", ctypes.c_int32), ("channels", c_void_p), ("values", c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("gain", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * (TQ_MAX_ROT_DIM // 2))]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("in_", c_void_p), ("out", c_void_p), ("weight", c_void_p), ("heads", ctypes.c_int32),
+                ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CacheBufs(ctypes.Structure):
+    _fields_ = [("k_codes", c_void_p), ("k_norms", c_void_p), ("v_codes", c_void_p), ("v_norms", c_void_p),
+                ("values", c_void_p), ("outliers", ctypes.c_int32)]
 
 
 _P = ctypes.POINTER
@@ -81,6 +99,23 @@ SIGNATURES = {
     "tq_status_string": (ctypes.c_char_p, [c_int]),
 }
 
+# Every symbol include/tq_spec.h declares.
+c_double = ctypes.c_double
+SPEC_SIGNATURES = {
+    "tq_make_rope": (c_int, [c_int, c_int, c_double, c_int, c_double, c_double, c_double, c_double, _P(Rope)]),
+    "tq_qk_norm_rope": (c_int, [_P(Rope), c_int, c_int, c_int, _P(Rows), _P(Rows), _P(Rows), c_int, c_int, c_int,
+                                c_int, c_float, c_float, c_void_p, c_void_p, c_void_p]),
+    "tq_tree_masks": (c_int, [c_void_p, c_int, c_void_p, c_void_p]),
+    "tq_tree_workspace_size": (c_size_t, [_P(KVDesc), c_int, c_int]),
+    "tq_decode_attention_tree": (c_int, [_P(KVDesc), _P(Codebook), _P(Codebook), c_int, c_int, c_void_p, c_int,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_float, c_void_p, c_int, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "tq_cache_compact": (c_int, [_P(KVDesc), _P(CacheBufs), c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p]),
+    "tq_cache_copy": (c_int, [_P(KVDesc), _P(CacheBufs), _P(KVDesc), _P(CacheBufs), c_int, c_void_p, c_void_p,
+                              c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p]),
+}
+
 _lib = None
 
 
@@ -93,7 +128,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m quantized_decode_attention_tq_b200.build`"
                 " (there is no fallback implementation)")
         l = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **SPEC_SIGNATURES}.items():
             fn = getattr(l, name)
             fn.restype = res
             fn.argtypes = args

@@ -35,7 +35,7 @@ def _sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    return hs + [os.path.join(ROOT, "include", "tq.h")]
+    return hs + [os.path.join(ROOT, "include", h) for h in ("tq.h", "tq_spec.h")]
 
 
 def _stale(target: str, deps) -> bool:

@@ -7,6 +7,7 @@
 
 #include "../../include/tq.h"
 #include "tq_internal.h"
+#include "tq_spec_internal.h"
 
 namespace {
 
@@ -149,6 +150,9 @@ struct StepRows {
 }  // namespace
 
 namespace tq {
+
+void sign_bits(uint64_t seed, uint32_t mask[4]) { sign_mask(seed, mask); }
+int validate_desc(const tq_kv_desc* d) { return check_desc(d); }
 
 int validate_decode(const tq_kv_desc* desc, const tq_codebook* k_cb, const tq_codebook* v_cb,
                     int q_heads, int n_q, const void* q, int q_dtype, const uint8_t* k_codes,
