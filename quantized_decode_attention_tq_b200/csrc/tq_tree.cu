@@ -4,129 +4,1227 @@
 //   x_t = scale / 128 * sum_blk nK_t q^ . cK[idx_t],  t visible to j,
 //   w = softmax(x), o = s o H (sum_t w_t nV_t / 128 cV[idx_t]).
 //
-// One CTA per row: a tile of 128 positions is scored by 128 threads, then
-// each thread adds the tile to its dimension of the output.
+// Mapping.  A unit is a (sequence, kv-head, group of up to N query rows); the
+// rows of a kv-head (nodes x heads of the group) share its K and V.  All
+// 128-position tiles of all units are laid end to end and cut evenly over one
+// persistent CTA per SM.  Per tile, codes become fp16 once for all N rows:
+//   S^T [128 positions x N rows] = K^ [128 x D] . Q^T     (tcgen05, M = 128)
+//   O^T [128 dims x N rows]     += V^T [128 x 128] . P    per 128-block
+// Positions are the MMA's rows, so N adapts to the tree (16 to 128 columns), a
+// thread owns one position (its two norms are registers), and both operands
+// made from codes are written in the cache's own order: K^ as K-major rows,
+// V^ as M-major rows, P as N-major rows, 128-byte swizzled.
+//
+// Softmax in the log2 domain with a lazy reference maximum per row: a tile is
+// scored against it, and only when some score exceeds it by 2^kTau do the
+// warps reduce the tile's maxima and rescale O in tensor memory.  The norm of
+// V multiplies the weight, scaled by a power of two so that fp16 holds it.
+//
+// Roundings to fp16, all others are fp32: the query is split in two fp16 terms
+// (two MMAs), the centroids are scaled by a factor that makes their rounding
+// small (centroid_scale), and weight * norm is rounded once.
+//
+// Warps: 0-7 softmax (two groups of 128 threads, half the rows each), 8-11 K
+// and 12-15 V from codes to fp16, 16 issues the MMAs.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
+#include <cstring>
+#include <type_traits>
+
 #include "tq_spec_internal.h"
 
 namespace tq {
+namespace tree {
 namespace {
 
-constexpr int kTreeTile = 128;
+constexpr int kTok = 128;           // positions per tile
+constexpr int kWarps = 17;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSoftWarps = 8;
+constexpr int kMaxGrid = 256;       // CTAs at most (slots of the workspace)
+constexpr uint32_t kBase = 1024;    // shared-window address of dynamic shared memory
+constexpr uint32_t kMaxDyn = 227 * 1024;
+constexpr float kTau = 6.0f;        // log2: how far a score may exceed the reference maximum
+constexpr float kUnset = -1e30f;    // reference of a row that has seen no position
+constexpr float kNormRoom = 512.0f; // V norms up to 2^9 times the unit's scale: 2^(6+9) fits fp16
+constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element x 128-row panel
 
-__device__ __forceinline__ float load_q(const TreeParams& p, size_t i) {
-  if (p.q_dtype == TQ_F32) return static_cast<const float*>(p.q)[i];
-  if (p.q_dtype == TQ_F16) return __half2float(static_cast<const __half*>(p.q)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[i]);
+struct Plan {
+  uint32_t bytes;
+  uint32_t q, kt, vt, pt;       // Q^ (hi, lo), K^ and V^ stages, P
+  uint32_t lut_k, lut_v;
+  uint32_t ring[8];             // code rings of the eight dequantising warps
+  uint32_t bar, misc, prefix;
+  int k_stages, v_stages, depth;
+};
+
+struct Params {
+  TreeParams t;
+  Plan pl;
+  float kscale, vscale;         // centroid scales
+  int n_hg;                     // row groups per kv-head
+  int* ws_prefix;               // [batch + 1]
+  float* ws_ml;                 // [2 * grid][N][2]
+  float* ws_acc;                // [2 * grid][N][D]
+};
+
+// ------------------------------------------------------------- primitives --
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
+  return x;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+  return x;
+}
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a));
+  return x;
+}
+// a code table never changes after the prologue: the compiler may move these
+__device__ __forceinline__ uint32_t lds_table(uint32_t a) {
+  uint32_t x;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
+  return x;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait(int pending) {
+  if (pending >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-__device__ __forceinline__ uint32_t code_at(const uint8_t* row, int bits, int i) {
-  const int bit = bits * i;
-  uint32_t w = row[bit >> 3];
-  if ((bit & 7) + bits > 8) w |= (uint32_t)row[(bit >> 3) + 1] << 8;
-  return (w >> (bit & 7)) & ((1u << bits) - 1u);
+__device__ __forceinline__ void bar_init(uint32_t a, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t a) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t a, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(a), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Wait for a phase, for at most about a second: then the abort word is set,
+// every later wait returns at once, the loops run to their end on whatever the
+// buffers hold (all accesses stay in bounds), and the status word says so.
+__device__ __forceinline__ void bar_wait(uint32_t a, uint32_t parity, uint32_t abort_word, uint32_t* status) {
+  if (bar_try(a, parity)) return;
+  const long long begin = clock64();
+  for (int i = 0; i < (1 << 26); ++i) {
+    if (bar_try(a, parity)) return;
+    if (lds32(abort_word)) return;
+    if (clock64() - begin > 2000000000LL) break;
+  }
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(abort_word), "r"(1) : "memory");
+  if (status) atomicOr(status, TQ_DEV_INTERNAL);
 }
 
-__device__ void block_wht(float* x, int D, int tid) {  // 128 threads
-  for (int m = 1; m < kBlock; m <<= 1) {
-    __syncthreads();
-    float r[2];
-    for (int k = 0; k * kBlock < D; ++k) {
-      const float a = x[k * kBlock + tid], b = x[k * kBlock + (tid ^ m)];
-      r[k] = (tid & m) ? b - a : a + b;
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_or(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %3, 0; bar.red.or.pred q, %1, %2, p; selp.b32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: K-major operands step
+// 1024 bytes per 8 rows (sbo); MN-major ones 1024 bytes per 8 k (sbo) and one
+// panel per 64 rows or columns (lbo).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16, fp16 operands, fp32 accumulator, M = 128
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int C>
+__device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[C]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  if constexpr (C == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(addr));
+  } else if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr));
+  } else {
+    static_assert(C == 32, "column chunk");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+  }
+}
+template <int C>
+__device__ __forceinline__ void tm_store(uint32_t addr, const float (&r)[C]) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+  if constexpr (C == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+  } else {
+    static_assert(C == 32, "column chunk");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+        "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+        "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+        : "memory");
+  }
+}
+
+// Unnormalised Walsh-Hadamard transform of the 128-blocks of one row held by a
+// warp (lane l: elements 4l..4l+3 of every block).
+template <int NB>
+__device__ __forceinline__ void wht(float (&v)[NB][4], int lane) {
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk) {
+    const float t0 = v[blk][0] + v[blk][1], t1 = v[blk][0] - v[blk][1];
+    const float t2 = v[blk][2] + v[blk][3], t3 = v[blk][2] - v[blk][3];
+    v[blk][0] = t0 + t2;
+    v[blk][2] = t0 - t2;
+    v[blk][1] = t1 + t3;
+    v[blk][3] = t1 - t3;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float o = __shfl_xor_sync(0xffffffffu, v[blk][k], m);
+        v[blk][k] = (lane & m) ? o - v[blk][k] : v[blk][k] + o;
+      }
+  }
+}
+
+// ------------------------------------------------------------------ split --
+
+// The flattened tiles [0, T) are cut into `parts` ranges of equal size.
+struct Cut {
+  const int* prefix;  // tiles before each batch entry
+  int batch, ub;      // ub: units per batch entry
+  long long total, parts;
+  __device__ Cut(const int* pre, int b, int units, int grid) : prefix(pre), batch(b), ub(units) {
+    total = (long long)pre[b] * units;
+    parts = min((long long)grid, total);
+  }
+  __device__ long long start(long long c) const { return c >= parts ? total : c * total / parts; }
+};
+
+struct Seg {
+  int b, r, kvh, hg, nt, lo, hi;
+  long long begin;  // first tile of the unit
+};
+__device__ __forceinline__ Seg find(const Cut& cut, long long x, long long end, int n_hg) {
+  int lo = 0, hi = cut.batch;  // the last entry whose tiles start at or before x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)cut.prefix[mid] * cut.ub <= x) lo = mid;
+    else hi = mid;
+  }
+  Seg s;
+  s.b = lo;
+  s.nt = cut.prefix[lo + 1] - cut.prefix[lo];
+  const long long first = (long long)cut.prefix[lo] * cut.ub;
+  s.r = (int)((x - first) / s.nt);
+  s.kvh = s.r / n_hg;
+  s.hg = s.r % n_hg;
+  s.begin = first + (long long)s.r * s.nt;
+  s.lo = (int)(x - s.begin);
+  s.hi = (int)min(end - s.begin, (long long)s.nt);
+  return s;
+}
+
+// ------------------------------------------------------------ codes -> fp16 --
+
+// Address of pair q (codes 2q, 2q + 1) of a B-bit stream in the lane's table:
+// entry f of lane l at table + f * 128 + 4 l, the table aligned to its size.
+template <int B>
+__device__ __forceinline__ uint32_t pair_addr(const uint32_t* w, int q, uint32_t lane_base) {
+  const int pos = 2 * B * q, wi = pos >> 5, sh = pos & 31;
+  uint32_t x;
+  if (sh + 2 * B > 32) x = __funnelshift_r(w[wi], w[wi + 1], sh - 7);
+  else x = sh >= 7 ? w[wi] >> (sh - 7) : w[wi] << (7 - sh);
+  return (x & (((1u << (2 * B)) - 1u) << 7)) | lane_base;
+}
+
+template <int B>
+struct Slot {  // a ring slot: 32 positions, one block; padded so that 128-bit reads of 8 lanes hit distinct banks
+  static constexpr int kStride = B == 4 ? 80 : 48;
+};
+__host__ __device__ constexpr uint32_t slot_bytes(int bits) { return 32u * (bits == 4 ? 80u : 48u); }
+
+// The values of one position and block: 64 pairs, written as 16 chunks of 8 fp16.
+template <int B>
+__device__ __forceinline__ void expand_row(uint32_t slot_row, uint32_t dst_row, int tok, uint32_t lane_base) {
+  uint32_t w[4 * B];
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    const uint4 x = lds128(slot_row + 16u * i);
+    w[4 * i] = x.x;
+    w[4 * i + 1] = x.y;
+    w[4 * i + 2] = x.z;
+    w[4 * i + 3] = x.w;
+  }
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lds_table(pair_addr<B>(w, 4 * c + i, lane_base));
+    sts128(dst_row + (uint32_t)(c >> 3) * kPanel + (uint32_t)(((c & 7) ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
+  }
+}
+
+// ------------------------------------------------------------------ output --
+
+// One row of the output: acc / (128 l), rotated back.  v holds acc / 128.
+template <int NB>
+__device__ __forceinline__ void emit_row(const TreeParams& p, float (&v)[NB][4], float l, int lane, size_t row) {
+  wht<NB>(v, lane);
+  const uint32_t sgn = p.sign_mask[lane >> 3] >> (4 * (lane & 7));
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // l = 0: no position seen
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk) {
+    float o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = l != 0.0f ? (((sgn >> k) & 1u) ? -v[blk][k] : v[blk][k]) * inv : 0.0f;
+    uint2 w;
+    if (p.out_dtype == TQ_F16) {
+      const __half2 a = __floats2half2_rn(o[0], o[1]), b = __floats2half2_rn(o[2], o[3]);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    __syncthreads();
-    for (int k = 0; k * kBlock < D; ++k) x[k * kBlock + tid] = r[k];
+    *reinterpret_cast<uint2*>(static_cast<char*>(p.out) + (row * NB * kBlock + blk * kBlock + 4 * lane) * 2) = w;
+  }
+}
+
+__device__ __forceinline__ int clamp_nodes(const TreeParams& p, int b) {
+  return p.n_nodes ? min(max(__ldg(p.n_nodes + b), 0), p.n_q) : p.n_q;
+}
+// The output row of column n of a row group, or -1.
+__device__ __forceinline__ long long out_row(const TreeParams& p, int b, int kvh, int vl, int nodes) {
+  const int G = p.q_heads / p.kv_heads;
+  const int j = vl / G;
+  if (j >= nodes) return -1;
+  return ((long long)b * p.n_q + j) * p.q_heads + kvh * G + (vl - j * G);
+}
+
+// --------------------------------------------------------------- the kernel --
+
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 13, kQFull = 14, kBars = 15 };
+
+// word offsets in the misc area
+template <int N>
+struct Misc {
+  static constexpr int kAbort = 0, kTmem = 1, kAnyEmpty = 2, kQmax = 4;      // [8]
+  static constexpr int kVmax = kQmax + 8;                                    // [8]
+  static constexpr int kMoff = kVmax + 8;                                    // [N]
+  static constexpr int kAlpha = kMoff + N;                                   // [N]
+  static constexpr int kRed = kAlpha + N;                                    // [4][N]
+  static constexpr int kMask = kRed + 4 * N;                                 // [N] 64-bit
+  static constexpr int kScan = kMask + 2 * N;                                // [16]
+  static constexpr int kWords = kScan + 16;
+};
+
+template <int NB, int N>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Params P) {
+  constexpr int D = NB * kBlock;
+  constexpr int HC = N / 2;                 // rows (columns of S) of a softmax group
+  constexpr int CH = HC < 32 ? HC : 32;     // columns per tensor-memory load
+  constexpr uint32_t kCols = 3 * NB * N <= 64 ? 64 : 3 * NB * N <= 128 ? 128 : 3 * NB * N <= 256 ? 256 : 512;
+  static_assert(3 * NB * N <= 512, "tensor memory");
+  constexpr uint32_t kQPanel = N * 128;     // bytes of a 64-dim panel of Q^
+  using M = Misc<N>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const TreeParams& p = P.t;
+  const Plan& pl = P.pl;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  {
+    uint32_t dyn;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
+    if (smem_u32(smem) != kBase || dyn < pl.bytes) {  // another layout of the shared window: reported, never used
+      if (tid == 0 && p.status) atomicOr(p.status, TQ_DEV_INTERNAL);
+      return;
+    }
+  }
+  auto gen = [&](uint32_t a) { return smem + (a - kBase); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(gen(pl.misc));
+  float* miscf = reinterpret_cast<float*>(misc);
+  int* prefix = reinterpret_cast<int*>(gen(pl.prefix));
+  const uint32_t abort_word = pl.misc + 4 * M::kAbort;
+  auto bar = [&](int i) { return pl.bar + 8u * (uint32_t)i; };
+  auto wait = [&](int i, uint32_t parity) { bar_wait(bar(i), parity, abort_word, p.status); };
+
+  // ---- set-up: barriers, tensor memory, code tables, lengths ----------------
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      bar_init(bar(kKFull + s), 4);
+      bar_init(bar(kKEmpty + s), 1);
+      bar_init(bar(kVFull + s), 4);
+      bar_init(bar(kVEmpty + s), 1);
+      bar_init(bar(kSFull + s), 1);
+      bar_init(bar(kSEmpty + s), kSoftWarps);
+    }
+    bar_init(bar(kPFull), kSoftWarps);
+    bar_init(bar(kPFree), 1);
+    bar_init(bar(kQFull), kSoftWarps);
+    misc[M::kAbort] = 0;
+    misc[M::kAnyEmpty] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 16) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(pl.misc + 4 * M::kTmem),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  int lens_r[4], local = 0;  // kMaxBatch / 512
+  const int per = (p.batch + 511) / 512;
+  if (tid < 512) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lens_r[i] = (i < per && tid * per + i < p.batch) ? __ldg(p.seq_lens + tid * per + i) : 0;
+  }
+  auto fill = [&](int bits, const float* cent, float scale, uint32_t base) {
+    const int n = 32 << (2 * bits), m = (1 << bits) - 1;
+    for (int e = tid; e < n; e += kThreads) {
+      const int f = e >> 5;
+      const __half2 h = __floats2half2_rn(cent[f & m] * scale, cent[f >> bits] * scale);
+      *reinterpret_cast<__half2*>(gen(base + 4u * (uint32_t)e)) = h;
+    }
+  };
+  fill(p.k_bits, p.kcent, P.kscale, pl.lut_k);
+  fill(p.v_bits, p.vcent, P.vscale, pl.lut_v);
+  bool empty = false;
+  if (tid < 512) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= per || tid * per + i >= p.batch) break;
+      const int len = min(max(lens_r[i], 0), p.seq_cap);
+      if (blockIdx.x == 0 && p.status) {
+        const int nn = p.n_nodes ? __ldg(p.n_nodes + tid * per + i) : 0;
+        if (len != lens_r[i] || nn < 0 || nn > p.n_q) atomicOr(p.status, TQ_DEV_LEN_RANGE);
+      }
+      lens_r[i] = (len + kTok - 1) / kTok;
+      local += lens_r[i];
+      empty |= len == 0;
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) misc[M::kScan + warp] = (uint32_t)incl;
+    local = incl - local;  // before this thread, inside the warp
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (tid < 512) {
+    int run = local;
+    for (int w = 0; w < warp; ++w) run += (int)misc[M::kScan + w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= per || tid * per + i >= p.batch) break;
+      prefix[tid * per + i] = run;
+      run += lens_r[i];
+      if (tid * per + i == p.batch - 1) prefix[p.batch] = run;
+    }
+    if (empty) misc[M::kAnyEmpty] = 1;
   }
   __syncthreads();
+  const uint32_t tmem = misc[M::kTmem];
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= p.batch; i += kThreads) P.ws_prefix[i] = prefix[i];
+
+  const int ub = p.kv_heads * P.n_hg;
+  const Cut cut(prefix, p.batch, ub, gridDim.x);
+  const long long begin = cut.start(blockIdx.x), end = blockIdx.x < cut.parts ? cut.start(blockIdx.x + 1) : begin;
+  const uint32_t tm_o = tmem + 2 * NB * N;  // O columns follow the two S stages
+
+  if (warp < kSoftWarps) {
+    // ================================================================ softmax
+    const int quad = warp & 3, grp = warp >> 2, tk = 32 * quad + lane;
+    const int c0 = grp * HC;  // first column of this group
+    const uint32_t tm_lane = (uint32_t)(32 * quad) << 16;
+    const uint32_t moff_a = pl.misc + 4u * (M::kMoff + c0), alpha_a = pl.misc + 4u * (M::kAlpha + c0);
+    const uint32_t mask_a = pl.misc + 4u * (M::kMask + 2 * c0);
+    float* red = miscf + M::kRed;  // [quad][N]
+    const int gid = 2 + grp;       // named barrier of the group
+    uint32_t tile_no = 0, seg_no = 0;  // across segments
+    const int G = p.q_heads / p.kv_heads;
+    for (long long x = begin; x < end; ++seg_no) {
+      const Seg sg = find(cut, x, end, P.n_hg);
+      const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
+      const int nodes = clamp_nodes(p, sg.b), ctx = len - nodes;
+      const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
+      // ---- the unit's rows: q^ = H (s o q), one power-of-two scale for all,
+      // split into two fp16 terms; column masks
+      named_sync(1, 32 * kSoftWarps);  // both groups are done with the unit before
+      float mul;
+      {
+        constexpr int RW = N / kSoftWarps;  // rows per warp
+        float v[RW][NB][4];
+        const uint32_t sgn = p.sign_mask[lane >> 3] >> (4 * (lane & 7));
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const int n = warp + kSoftWarps * i, vl = sg.hg * N + n;
+          const long long row = vl < G * p.n_q ? out_row(p, sg.b, sg.kvh, vl, nodes) : -1;
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            v[i][blk][0] = v[i][blk][1] = v[i][blk][2] = v[i][blk][3] = 0.0f;
+            if (row >= 0) {
+              const size_t e = (size_t)row * D + blk * kBlock + 4 * lane;
+              if (p.q_dtype == TQ_F32) {
+                const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
+                v[i][blk][0] = a.x; v[i][blk][1] = a.y; v[i][blk][2] = a.z; v[i][blk][3] = a.w;
+              } else {
+                const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + e);
+                float2 a, c;
+                if (p.q_dtype == TQ_F16) {
+                  a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+                  c = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+                } else {
+                  a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.x));
+                  c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.y));
+                }
+                v[i][blk][0] = a.x; v[i][blk][1] = a.y; v[i][blk][2] = c.x; v[i][blk][3] = c.y;
+              }
+            }
+          }
+          if (lane == 0)
+            *reinterpret_cast<uint64_t*>(misc + M::kMask + 2 * n) =
+                row >= 0 ? __ldg(reinterpret_cast<const unsigned long long*>(p.tree) + (size_t)sg.b * p.n_q + vl / G) : 0ull;
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if ((sgn >> k) & 1u) v[i][blk][k] = -v[i][blk][k];
+          wht<NB>(v[i], lane);
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = fabsf(v[i][blk][k]);
+              mx = fmaxf(mx, a < INFINITY ? a : 0.0f);  // rows that are not finite have no say
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (lane == 0) miscf[M::kQmax + warp] = mx;
+        named_sync(1, 32 * kSoftWarps);
+#pragma unroll
+        for (int w = 0; w < kSoftWarps; ++w) mx = fmaxf(mx, miscf[M::kQmax + w]);
+        const int qe = mx > 0.0f ? max(ilogbf(mx) - 13, -110) : 0;
+        const float sc = ldexpf(1.0f, -qe);
+        mul = p.score_mult * ldexpf(1.0f, qe) / P.kscale;
+        // lane l holds dims 4l..4l+3: chunk l / 2 of the block, half l & 1
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const int n = warp + kSoftWarps * i;
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            const uint32_t a = pl.q + (uint32_t)(2 * blk + (lane >> 4)) * kQPanel + (uint32_t)n * 128u +
+                               (uint32_t)((((lane >> 1) & 7) ^ (n & 7)) << 4) + 8u * (lane & 1);
+            float y[4];
+            __half2 h[2], r[2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = v[i][blk][k] * sc;
+            h[0] = __floats2half2_rn(y[0], y[1]);
+            h[1] = __floats2half2_rn(y[2], y[3]);
+            const float2 b0 = __half22float2(h[0]), b1 = __half22float2(h[1]);
+            r[0] = __floats2half2_rn(y[0] - b0.x, y[1] - b0.y);
+            r[1] = __floats2half2_rn(y[2] - b1.x, y[3] - b1.y);
+            sts64(a, *reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]));
+            sts64(a + 2 * NB * kQPanel, *reinterpret_cast<uint32_t*>(&r[0]), *reinterpret_cast<uint32_t*>(&r[1]));
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(kQFull));
+      }
+      if (tk < HC) miscf[M::kMoff + c0 + tk] = kUnset;
+      named_sync(gid, 128);
+      float l[HC];
+#pragma unroll
+      for (int c = 0; c < HC; ++c) l[c] = 0.0f;
+      float vpow = 1.0f;  // 2^-e of the V norms, e the unit's scale
+      // this thread's norms of the next tile
+      float kn[NB], vn[NB];
+      auto load_norms = [&](int tile) {
+        const int t = tile * kTok + tk;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          kn[blk] = vn[blk] = 0.0f;
+          if (t < len) {
+            kn[blk] = __half2float(__ushort_as_half(__ldg(p.k_norms + (row0 + t) * NB + blk)));
+            vn[blk] = __half2float(__ushort_as_half(__ldg(p.v_norms + (row0 + t) * NB + blk)));
+          }
+        }
+      };
+      load_norms(sg.lo);
+      for (int tile = sg.lo; tile < sg.hi; ++tile, ++tile_no) {
+        const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
+        float f[NB], v_n[NB];
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          f[blk] = kn[blk] * mul;
+          v_n[blk] = vn[blk];
+        }
+        if (tile + 1 < sg.hi) load_norms(tile + 1);
+        const int t = tile * kTok + tk, node = t - ctx;
+        const bool masked = (tile + 1) * kTok > ctx;  // the tile holds drafted nodes or the end
+        const uint32_t tm_s = tmem + tm_lane + st * (NB * N) + c0;
+        wait(kSFull + st, ph);
+        tc_after();
+        // score of column c of the chunk, against no reference
+        auto load_scores = [&](int ch, float (&s)[CH]) {
+          tm_load<CH>(tm_s + ch * CH, s);
+          if constexpr (NB == 2) {
+            float s1[CH];
+            tm_load<CH>(tm_s + N + ch * CH, s1);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) s[c] = fmaf(s1[c], f[NB - 1], s[c] * f[0]);
+          } else {
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) s[c] *= f[0];
+          }
+        };
+        auto sees = [&](int c) {  // does row c0 + c see this thread's position
+          uint64_t w;
+          asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(mask_a + 8u * c));
+          return t < len && (node < 0 || ((w >> node) & 1ull));
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < HC / CH; ++ch) {
+          float s[CH];
+          load_scores(ch, s);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+              if (!sees(ch * CH + c)) s[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < CH; c += 4) {
+            const float4 m = lds128f(moff_a + 4u * (ch * CH + c));
+            top = fmaxf(top, fmaxf(fmaxf(s[c] - m.x, s[c + 1] - m.y), fmaxf(s[c + 2] - m.z, s[c + 3] - m.w)));
+          }
+        }
+        float vbig = 0.0f;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) vbig = fmaxf(vbig, v_n[blk] < INFINITY ? v_n[blk] : 0.0f);
+        const bool need = top > kTau || vbig * vpow > kNormRoom;
+        if (named_or(gid, 128, need)) {
+          // ---- new reference maxima and V scale: maxima of the tile per row
+#pragma unroll
+          for (int ch = 0; ch < HC / CH; ++ch) {
+            float s[CH];
+            load_scores(ch, s);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              float y = s[c];
+              if (masked && !sees(ch * CH + c)) y = -INFINITY;
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+              if (lane == 0) red[quad * N + c0 + ch * CH + c] = y;
+            }
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) vbig = fmaxf(vbig, __shfl_xor_sync(0xffffffffu, vbig, o));
+          if (lane == 0) miscf[M::kVmax + warp] = vbig;
+          named_sync(gid, 128);
+          if (tk < HC) {
+            const int c = c0 + tk;
+            const float y = fmaxf(fmaxf(red[c], red[N + c]), fmaxf(red[2 * N + c], red[3 * N + c]));
+            const float old = miscf[M::kMoff + c];
+            float a = 1.0f;
+            if (y > old + kTau) {
+              a = old == kUnset ? 0.0f : ex2(old - y);
+              miscf[M::kMoff + c] = y;
+            }
+            miscf[M::kAlpha + c] = a;
+          }
+          float vm = 0.0f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vm = fmaxf(vm, miscf[M::kVmax + 4 * grp + w]);
+          float beta = 1.0f;
+          if (vm > 0.0f && (tile == sg.lo || vm * vpow > kNormRoom)) {
+            const float np = ldexpf(1.0f, -ilogbf(vm));
+            beta = np / vpow;
+            vpow = np;
+          }
+          named_sync(gid, 128);
+          if (tile > sg.lo) {
+            wait(kPFree, (tile_no - 1) & 1);  // the sum so far
+            tc_after();
+          }
+#pragma unroll
+          for (int ch = 0; ch < HC / CH; ++ch) {
+            float a[CH];
+#pragma unroll
+            for (int c = 0; c < CH; c += 4) {
+              const float4 m = lds128f(alpha_a + 4u * (ch * CH + c));
+              a[c] = m.x; a[c + 1] = m.y; a[c + 2] = m.z; a[c + 3] = m.w;
+            }
+#pragma unroll
+            for (int c = 0; c < CH; ++c) l[ch * CH + c] *= a[c];
+            if (tile > sg.lo) {
+#pragma unroll
+              for (int blk = 0; blk < NB; ++blk) {
+                float o[CH];
+                tm_load<CH>(tm_o + tm_lane + blk * N + c0 + ch * CH, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < CH; ++c) o[c] *= a[c] * beta;
+                tm_store<CH>(tm_o + tm_lane + blk * N + c0 + ch * CH, o);
+              }
+            }
+          }
+          tc_wait_st();
+        }
+        // ---- weights, their sums, and weight * norm as the MMA's operand
+        float vs[NB];
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) vs[blk] = v_n[blk] * vpow;
+        if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);
+#pragma unroll
+        for (int ch = 0; ch < HC / CH; ++ch) {
+          float s[CH];
+          load_scores(ch, s);
+          uint32_t hidden = 0;
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+              if (!sees(ch * CH + c)) hidden |= 1u << c;
+          }
+#pragma unroll
+          for (int c = 0; c < CH; c += 8) {
+            const float4 m0 = lds128f(moff_a + 4u * (ch * CH + c)), m1 = lds128f(moff_a + 4u * (ch * CH + c + 4));
+            const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              w[k] = ex2(s[c + k] - m[k]);
+              if (masked && ((hidden >> (c + k)) & 1u)) w[k] = 0.0f;
+              l[ch * CH + c + k] += w[k];
+            }
+            const int col = c0 + ch * CH + c;
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk) {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float a = w[2 * k] * vs[blk], b = w[2 * k + 1] * vs[blk];
+                if (masked) {  // a hidden position's norm may be anything
+                  if ((hidden >> (c + 2 * k)) & 1u) a = 0.0f;
+                  if ((hidden >> (c + 2 * k + 1)) & 1u) b = 0.0f;
+                }
+                const __half2 hh = __floats2half2_rn(a, b);
+                h[k] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+              sts128(pl.pt + (uint32_t)(blk * ((N + 63) / 64) + (col >> 6)) * kPanel + (uint32_t)tk * 128u +
+                         (uint32_t)((((col >> 3) & 7) ^ (tk & 7)) << 4),
+                     h[0], h[1], h[2], h[3]);
+            }
+          }
+        }
+        tc_before();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar(kSEmpty + st));
+          bar_arrive(bar(kPFull));
+        }
+      }
+      // ---- the segment's partial: l over the positions, O, reference maxima
+      wait(kPFree, (tile_no - 1) & 1);
+      tc_after();
+#pragma unroll
+      for (int c = 0; c < HC; ++c) {
+        float y = l[c];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (lane == 0) red[quad * N + c0 + c] = y;
+      }
+      named_sync(gid, 128);
+      const long long slot = 2 * (long long)blockIdx.x + (sg.lo == 0 ? 1 : 0);
+      float* ml = P.ws_ml + slot * N * 2;
+      float* acc = P.ws_acc + slot * N * D;
+      if (tk < HC) {
+        const int c = c0 + tk;
+        const float m = miscf[M::kMoff + c], sum = red[c] + red[N + c] + red[2 * N + c] + red[3 * N + c];
+        // a row with a NaN score keeps it through the join: its maximum is made infinite
+        *reinterpret_cast<float2*>(ml + 2 * c) = make_float2(sum != sum ? INFINITY : m == kUnset ? -INFINITY : m, sum);
+      }
+      const float osc = 1.0f / (vpow * P.vscale * kBlock);
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int ch = 0; ch < HC / CH; ++ch) {
+          float o[CH];
+          tm_load<CH>(tm_o + tm_lane + blk * N + c0 + ch * CH, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < CH; ++c) acc[(size_t)(c0 + ch * CH + c) * D + blk * kBlock + tk] = o[c] * osc;
+        }
+      tc_before();
+      if (sg.lo == 0 && sg.hi == sg.nt) {  // the whole unit: emit its rows
+        named_sync(1, 32 * kSoftWarps);
+        for (int n = warp; n < N; n += kSoftWarps) {
+          const int vl = sg.hg * N + n;
+          const long long row = vl < G * p.n_q ? out_row(p, sg.b, sg.kvh, vl, nodes) : -1;
+          if (row < 0) continue;
+          float v[NB][4];
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(acc + (size_t)n * D + blk * kBlock + 4 * lane));
+            v[blk][0] = a.x; v[blk][1] = a.y; v[blk][2] = a.z; v[blk][3] = a.w;
+          }
+          emit_row<NB>(p, v, __ldcg(ml + 2 * n + 1), lane, (size_t)row);
+        }
+      }
+      x = sg.begin + sg.hi;
+    }
+  } else if (warp < 16) {
+    // ============================================================ dequantise
+    const int dq = warp - 8, side = dq >> 2, quarter = dq & 3;
+    const uint32_t ring = pl.ring[dq];
+    auto work = [&](auto bits_tag) {
+      constexpr int B = decltype(bits_tag)::value;
+      constexpr int kStride = Slot<B>::kStride;
+      constexpr uint32_t kSlot = 32 * kStride;
+      const uint8_t* codes = side ? p.v_codes : p.k_codes;
+      const uint32_t lane_base = (side ? pl.lut_v : pl.lut_k) + 4u * lane;
+      const uint32_t stage0 = side ? pl.vt : pl.kt;
+      const int stages = side ? pl.v_stages : pl.k_stages, depth = pl.depth;
+      const int full = side ? kVFull : kKFull, emptyb = side ? kVEmpty : kKEmpty;
+      const int tok = 32 * quarter + lane;
+      uint32_t stage = 0, ephase = 1;  // the first round finds the stages free
+      int cslot = 0, islot = 0;
+      for (long long x = begin; x < end;) {
+        const Seg sg = find(cut, x, end, P.n_hg);
+        const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
+        const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
+        const int items = (sg.hi - sg.lo) * NB;
+        auto issue = [&](int item) {
+          if (item < items) {
+            const int t0 = (sg.lo + item / NB) * kTok + 32 * quarter, blk = item % NB;
+#pragma unroll
+            for (int r = 0; r < B; ++r) {
+              const int c = lane + 32 * r, tt = c / B, part = c % B;
+              const bool ok = t0 + tt < len;
+              const uint8_t* src = codes + ((row0 + (ok ? t0 + tt : 0)) * NB + blk) * (16 * B) + 16 * part;
+              cp_async16(ring + (uint32_t)islot * kSlot + (uint32_t)(tt * kStride + 16 * part), src, ok ? 16u : 0u);
+            }
+          }
+          cp_commit();
+          if (++islot == depth) islot = 0;
+        };
+        for (int i = 0; i < depth; ++i) issue(i);
+        for (int item = 0; item < items; ++item) {
+          cp_wait(depth - 1);
+          __syncwarp();
+          wait(emptyb + stage, ephase);
+          const uint32_t dst = stage0 + stage * 2 * kPanel + (uint32_t)tok * 128u;
+          expand_row<B>(ring + (uint32_t)cslot * kSlot + (uint32_t)(lane * kStride), dst, tok, lane_base);
+          if (++cslot == depth) cslot = 0;
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar(full + stage));
+          issue(item + depth);
+          if (++stage == (uint32_t)stages) {
+            stage = 0;
+            ephase ^= 1;
+          }
+        }
+        x = sg.begin + sg.hi;
+      }
+      cp_wait(0);
+    };
+    const int bits = side ? p.v_bits : p.k_bits;
+    if (bits == 2) work(std::integral_constant<int, 2>{});
+    else if (bits == 3) work(std::integral_constant<int, 3>{});
+    else work(std::integral_constant<int, 4>{});
+  } else {
+    // ================================================================= MMAs
+    constexpr uint32_t id_s = mma_desc(N, false, false), id_o = mma_desc(N, true, true);
+    uint32_t ks = 0, kph = 0, vs = 0, vph = 0, tile_no = 0, seg_no = 0;
+    const bool one = lane == 0;
+    auto pv = [&](uint32_t no, bool first) {
+      wait(kPFull, no & 1);
+      tc_after();
+      for (int blk = 0; blk < NB; ++blk) {
+        wait(kVFull + vs, vph);
+        tc_after();
+        if (one) {
+          const uint32_t a = pl.vt + vs * 2 * kPanel, b = pl.pt + (uint32_t)(blk * ((N + 63) / 64)) * kPanel;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma(tm_o + blk * N, smem_desc(a + 2048u * k, kPanel, 1024), smem_desc(b + 2048u * k, kPanel, 1024), id_o,
+                   first && k == 0 ? 0u : 1u);
+          tc_commit(bar(kVEmpty + vs));
+          if (blk == NB - 1) tc_commit(bar(kPFree));
+        }
+        __syncwarp();
+        if (++vs == (uint32_t)pl.v_stages) {
+          vs = 0;
+          vph ^= 1;
+        }
+      }
+    };
+    for (long long x = begin; x < end; ++seg_no) {
+      const Seg sg = find(cut, x, end, P.n_hg);
+      wait(kQFull, seg_no & 1);
+      for (int tile = sg.lo; tile < sg.hi; ++tile, ++tile_no) {
+        const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
+        wait(kSEmpty + st, ph ^ 1);
+        tc_after();
+        for (int blk = 0; blk < NB; ++blk) {
+          wait(kKFull + ks, kph);
+          tc_after();
+          if (one) {
+            const uint32_t a = pl.kt + ks * 2 * kPanel;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)  // the two terms of the query
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t b = pl.q + (uint32_t)(half * 2 * NB + 2 * blk + (k >> 2)) * kQPanel + 32u * (k & 3);
+                tc_mma(tmem + st * (NB * N) + blk * N, smem_desc(a + (uint32_t)(k >> 2) * kPanel + 32u * (k & 3), 16, 1024),
+                       smem_desc(b, 16, 1024), id_s, half == 0 && k == 0 ? 0u : 1u);
+              }
+            tc_commit(bar(kKEmpty + ks));
+            if (blk == NB - 1) tc_commit(bar(kSFull + st));
+          }
+          __syncwarp();
+          if (++ks == (uint32_t)pl.k_stages) {
+            ks = 0;
+            kph ^= 1;
+          }
+        }
+        if (tile > sg.lo) pv(tile_no - 1, tile - 1 == sg.lo);
+      }
+      pv(tile_no - 1, sg.hi - 1 == sg.lo);
+      x = sg.begin + sg.hi;
+    }
+    if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);  // nothing in flight when tensor memory is freed
+  }
+
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 16)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  // ---- rows of empty sequences are zero
+  if (misc[M::kAnyEmpty]) {
+    const long long rows = (long long)p.batch * p.n_q * p.q_heads;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+      const long long r = row / p.q_heads;
+      const int b = (int)(r / p.n_q), j = (int)(r % p.n_q);
+      if (prefix[b + 1] != prefix[b] || j >= clamp_nodes(p, b)) continue;
+      for (int d = tid; d < D; d += kThreads) static_cast<uint16_t*>(p.out)[row * D + d] = 0;
+    }
+  }
 }
 
-__global__ void __launch_bounds__(kTreeTile) tree_rows_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ float qs[kMaxDecodeHeadDim], os[kMaxDecodeHeadDim], ps[kTreeTile], red[4];
-  __shared__ float kc[16], vc[16];
-  const int tid = threadIdx.x, D = p.head_dim, nb = D / kBlock;
-  const int h = (int)(blockIdx.x % (unsigned)p.q_heads);
-  const int j = (int)(blockIdx.x / (unsigned)p.q_heads % (unsigned)p.n_q);
-  const int b = (int)(blockIdx.x / (unsigned)p.q_heads / (unsigned)p.n_q);
-  const int raw_len = p.seq_lens[b], raw_n = p.n_nodes ? p.n_nodes[b] : p.n_q;
-  const int len = min(max(raw_len, 0), p.seq_cap), n = min(max(raw_n, 0), p.n_q);
-  if ((len != raw_len || n != raw_n) && tid == 0 && p.status) atomicOr(p.status, TQ_DEV_LEN_RANGE);
-  if (j >= n) return;
-  const int ctx = len - n;
-  const uint64_t seen = p.tree[(size_t)b * p.n_q + j];
-  const size_t row = ((size_t)b * p.n_q + j) * p.q_heads + h;
-  const int kvh = h / (p.q_heads / p.kv_heads);
-  const size_t base = ((size_t)b * p.kv_heads + kvh) * p.seq_cap;
-  if (tid < 16) {
-    kc[tid] = p.kcent[tid];
-    vc[tid] = p.vcent[tid];
-  }
-  const bool neg = (p.sign_mask[tid >> 5] >> (tid & 31)) & 1u;
-  for (int k = 0; k < nb; ++k) {
-    const float x = load_q(p, row * D + k * kBlock + tid);
-    qs[k * kBlock + tid] = neg ? -x : x;
-  }
-  block_wht(qs, D, tid);
-  float m = -INFINITY, l = 0.0f, acc[2] = {0.0f, 0.0f};
-  for (int t0 = 0; t0 < len; t0 += kTreeTile) {
-    const int t = t0 + tid, node = t - ctx;
-    float x = -INFINITY;
-    const bool sees = t < len && (node < 0 || ((seen >> node) & 1u));
-    if (sees) {
-      x = 0.0f;
-      for (int k = 0; k < nb; ++k) {
-        const uint8_t* codes = p.k_codes + ((base + t) * nb + k) * 16 * p.k_bits;
-        float s = 0.0f;
-        for (int i = 0; i < kBlock; ++i) s = fmaf(qs[k * kBlock + i], kc[code_at(codes, p.k_bits, i)], s);
-        x = fmaf(s, __half2float(__ushort_as_half(p.k_norms[(base + t) * nb + k])), x);
+// Join of the units that a cut went through.  Block (c, g): boundary c of the
+// split, rows 8 g .. 8 g + 7; only a unit's first inner boundary does it.
+template <int NB, int N>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Params P, int grid) {
+  constexpr int D = NB * kBlock;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeParams& p = P.t;
+  const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Cut cut(P.ws_prefix, p.batch, p.kv_heads * P.n_hg, grid);
+  const long long c = blockIdx.x + 1;
+  if (c >= cut.parts) return;
+  const long long x = cut.start(c);
+  const Seg sg = find(cut, x, cut.total, P.n_hg);
+  if (sg.lo == 0 || cut.start(c - 1) > sg.begin) return;
+  const int vl = sg.hg * N + n;
+  if (vl >= p.q_heads / p.kv_heads * p.n_q) return;
+  const long long row = out_row(p, sg.b, sg.kvh, vl, clamp_nodes(p, sg.b));
+  if (row < 0) return;
+  // part c - 1 holds the unit's first tiles (its last segment: slot 2 (c-1) + 1),
+  // parts c, c + 1, ... the rest (their first segments: slots 2 c', ...)
+  long long last = c;
+  while (last + 1 < cut.parts && cut.start(last + 1) < sg.begin + sg.nt) ++last;
+  const int parts = (int)(last - c) + 2;
+  auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
+  float top = -INFINITY, l = 0.0f;
+  float v[NB][4] = {};
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int i = i0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (i < parts) ml = *reinterpret_cast<const float2*>(P.ws_ml + (slot(i) * N + n) * 2);
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(m, top);
+    const float down = top == -INFINITY ? 0.0f : ex2(top - m);
+    top = m;
+    const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+    float s = w != 0.0f ? ml.y * w : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    l = l * down + s;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[blk][k] *= down;
+    const int m_parts = min(32, parts - i0);
+#pragma unroll 4
+    for (int j = 0; j < m_parts; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float* acc = P.ws_acc + (slot(i0 + j) * N + n) * D + 4 * lane;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        const float4 a = *reinterpret_cast<const float4*>(acc + blk * kBlock);
+        if (wj != 0.0f) {
+          v[blk][0] = fmaf(a.x, wj, v[blk][0]);
+          v[blk][1] = fmaf(a.y, wj, v[blk][1]);
+          v[blk][2] = fmaf(a.z, wj, v[blk][2]);
+          v[blk][3] = fmaf(a.w, wj, v[blk][3]);
+        }
       }
-      x *= p.score_mult;
     }
-    float mx = x;
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float alpha = mx == -INFINITY ? 1.0f : exp2f(m - mx);
-    ps[tid] = !sees ? -1.0f : x == -INFINITY ? 0.0f : exp2f(x - mx);  // -1: not seen
-    m = mx;
-    __syncthreads();
-    l *= alpha;
-    for (int k = 0; k < nb; ++k) acc[k] *= alpha;
-    for (int i = 0; i < kTreeTile && t0 + i < len; ++i) {
-      const float w = ps[i];
-      if (w == -1.0f) continue;
-      l += w;
-      for (int k = 0; k < nb; ++k) {
-        const size_t r = (base + t0 + i) * nb + k;
-        const float nv = __half2float(__ushort_as_half(p.v_norms[r]));
-        acc[k] = fmaf(w * nv, vc[code_at(p.v_codes + r * 16 * p.v_bits, p.v_bits, tid)], acc[k]);
+  }
+  emit_row<NB>(p, v, l, lane, (size_t)row);
+}
+
+// --------------------------------------------------------------- host side --
+
+// A factor for a codebook's levels that makes their rounding to fp16 small:
+// the best of 256 in [1, 2), by the sum of squared errors.  The kernel divides
+// it out in fp32.
+float centroid_scale(const float* cent, int bits) {
+  const int half = 1 << (bits - 1);
+  float best = 1.0f, least = INFINITY;
+  for (int k = 0; k < 256; ++k) {
+    const float a = 1.0f + k * (1.0f / 256.0f);
+    float err = 0.0f;
+    for (int j = 0; j < half; ++j) {
+      const float x = cent[half + j] * a;
+      uint32_t u;
+      memcpy(&u, &x, 4);
+      u = (u + 0xFFFu + ((u >> 13) & 1u)) & ~0x1FFFu;  // 10 mantissa bits, to nearest even
+      float r;
+      memcpy(&r, &u, 4);
+      err += (r - x) * (r - x);
+    }
+    err /= a * a;
+    if (err < least) {
+      least = err;
+      best = a;
+    }
+  }
+  return best;
+}
+
+// First-fit placement in the shared window.
+struct Place {
+  uint32_t lo[16], hi[16];
+  int n = 1;
+  Place() { lo[0] = kBase, hi[0] = kBase + kMaxDyn; }
+  uint32_t take(uint32_t size, uint32_t align) {
+    for (int i = 0; i < n; ++i) {
+      const uint32_t a = (lo[i] + align - 1) / align * align;
+      if (a + size > hi[i]) continue;
+      const uint32_t l0 = lo[i];
+      lo[i] = a + size;
+      if (a > l0 && n < 16) {
+        for (int j = n; j > i; --j) lo[j] = lo[j - 1], hi[j] = hi[j - 1];
+        lo[i] = l0;
+        hi[i] = a;
+        ++n;
       }
+      return a;
     }
-    __syncthreads();
+    return 0;
   }
-  for (int k = 0; k < nb; ++k) os[k * kBlock + tid] = acc[k];
-  block_wht(os, D, tid);
-  const float inv = l > 0.0f || l != l ? 1.0f / (l * kBlock) : 0.0f;
-  for (int k = 0; k < nb; ++k) {
-    const float x = os[k * kBlock + tid] * (neg ? -inv : inv);
-    if (p.out_dtype == TQ_F16) static_cast<__half*>(p.out)[row * D + k * kBlock + tid] = __float2half_rn(x);
-    else static_cast<__nv_bfloat16*>(p.out)[row * D + k * kBlock + tid] = __float2bfloat16_rn(x);
+};
+
+template <int NB, int N>
+bool plan(const TreeParams& p, Plan& pl) {
+  // in order of preference: stages of K^ and V^, slots of a code ring
+  static const int tries[6][3] = {{2, 2, 3}, {2, 2, 2}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}};
+  for (const auto& t : tries) {
+    pl = Plan{};
+    Place at;
+    uint32_t end = 0;
+    bool ok = true;
+    auto take = [&](uint32_t size, uint32_t align) {
+      const uint32_t a = at.take(size, align);
+      ok = ok && a != 0;
+      if (a + size > end) end = a + size;
+      return a;
+    };
+    pl.k_stages = t[0];
+    pl.v_stages = t[1];
+    pl.depth = t[2];
+    pl.lut_k = take(128u << (2 * p.k_bits), 128u << (2 * p.k_bits));
+    pl.lut_v = take(128u << (2 * p.v_bits), 128u << (2 * p.v_bits));
+    pl.kt = take(2 * kPanel * t[0], 1024);
+    pl.vt = take(2 * kPanel * t[1], 1024);
+    pl.q = take((uint32_t)(4 * NB * N * 128), 1024);
+    pl.pt = take((uint32_t)(NB * ((N + 63) / 64)) * kPanel, 1024);
+    for (int w = 0; w < 8; ++w) pl.ring[w] = take(slot_bytes(w < 4 ? p.k_bits : p.v_bits) * t[2], 128);
+    pl.bar = take(8 * kBars, 128);
+    pl.misc = take(4 * Misc<N>::kWords, 128);
+    pl.prefix = take(4u * (uint32_t)(p.batch + 1), 128);
+    pl.bytes = end - kBase;
+    if (ok) return true;
   }
+  return false;
+}
+
+int sm_count(int* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
+  if (cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return TQ_ERR_CUDA;
+  return TQ_OK;
+}
+
+template <int NB, int N>
+int run(Params& P, cudaStream_t stream) {
+  const TreeParams& p = P.t;
+  const int rows = p.q_heads / p.kv_heads * p.n_q;
+  P.n_hg = (rows + N - 1) / N;
+  const long long tiles =
+      (long long)p.batch * p.kv_heads * P.n_hg * ((p.seq_cap + kTok - 1) / kTok);
+  int sms = 0;
+  if (sm_count(&sms) != TQ_OK) return TQ_ERR_CUDA;
+  const int grid = (int)min(min((long long)sms, (long long)kMaxGrid), tiles);
+  char* ws = static_cast<char*>(p.workspace);
+  P.ws_prefix = reinterpret_cast<int*>(ws);
+  ws += ((size_t)(p.batch + 1) * 4 + 255) / 256 * 256;
+  P.ws_ml = reinterpret_cast<float*>(ws);
+  ws += (size_t)2 * kMaxGrid * N * 2 * 4;
+  P.ws_acc = reinterpret_cast<float*>(ws);
+  auto kern = tree_kernel<NB, N>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  kern<<<grid, kThreads, P.pl.bytes, stream>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  if (grid == 1) return TQ_OK;  // no cut
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(grid - 1), N / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, merge_kernel<NB, N>, P, grid) != cudaSuccess) return TQ_ERR_CUDA;
+  return TQ_OK;
+}
+
+// The narrowest N that holds a kv-head's rows, or else the widest that fits.
+template <int NB, int N>
+int pick(Params& P, cudaStream_t stream) {
+  const int rows = P.t.q_heads / P.t.kv_heads * P.t.n_q;
+  if constexpr (N < (NB == 1 ? 128 : 64)) {
+    if (rows > N) {
+      const int st = pick<NB, 2 * N>(P, stream);
+      if (st != TQ_ERR_UNSUPPORTED) return st;
+    }
+  }
+  if (!plan<NB, N>(P.t, P.pl)) return TQ_ERR_UNSUPPORTED;
+  return run<NB, N>(P, stream);
 }
 
 }  // namespace
+}  // namespace tree
 
-size_t tree_workspace_bytes(int, int, int, int, int) { return 256; }
+size_t tree_workspace_bytes(int batch, int head_dim) {
+  // the widest row group's slots: N * head_dim is 128 * 128 at most
+  const size_t n = head_dim == kBlock ? 128 : 64;
+  return ((size_t)(batch + 1) * 4 + 255) / 256 * 256 + (size_t)2 * tree::kMaxGrid * n * (head_dim + 2) * 4;
+}
 
-int launch_tree(const TreeParams& p, cudaStream_t stream) {
-  const long long rows = (long long)p.batch * p.n_q * p.q_heads;
-  if (rows >= (1LL << 31)) return TQ_ERR_UNSUPPORTED;
-  tree_rows_kernel<<<(unsigned)rows, kTreeTile, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+int launch_tree(const TreeParams& t, cudaStream_t stream) {
+  tree::Params P{};
+  P.t = t;
+  P.kscale = tree::centroid_scale(t.kcent, t.k_bits);
+  P.vscale = tree::centroid_scale(t.vcent, t.v_bits);
+  return t.head_dim == kBlock ? tree::pick<1, 16>(P, stream) : tree::pick<2, 16>(P, stream);
 }
 
 }  // namespace tq
