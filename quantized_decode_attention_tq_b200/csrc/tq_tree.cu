@@ -25,7 +25,7 @@
 // small (centroid_scale), and weight * norm is rounded once.
 //
 // Warps: 0-7 softmax (two groups of 128 threads, half the rows each), 8-11 K
-// and 12-15 V from codes to fp16, 16 issues the MMAs.
+// and 12-15 V from codes to fp16, 16 and 17 issue the MMAs (18 and 19 idle).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,8 +41,12 @@ namespace tree {
 namespace {
 
 constexpr int kTok = 128;           // positions per tile
-constexpr int kWarps = 17;
+constexpr int kWarps = 20;          // five warpgroups, for the register split
 constexpr int kThreads = 32 * kWarps;
+// Registers per thread: at launch, then of the softmax (two warpgroups), the
+// dequantising (two) and the MMA warpgroup.  The shares must fit the launch's.
+constexpr int kRegsLaunch = 96, kRegsSoft = 136, kRegsCodes = 72, kRegsMma = 64;
+static_assert(2 * kRegsSoft + 2 * kRegsCodes + kRegsMma <= 5 * kRegsLaunch, "register split");
 constexpr int kSoftWarps = 8;
 constexpr int kMaxGrid = 256;       // CTAs at most (slots of the workspace)
 constexpr uint32_t kBase = 1024;    // shared-window address of dynamic shared memory
@@ -66,6 +70,7 @@ struct Params {
   Plan pl;
   float kscale, vscale;         // centroid scales
   int n_hg;                     // row groups per kv-head
+  FastDiv group;                // q_heads / kv_heads
   int* ws_prefix;               // [batch + 1]
   float* ws_ml;                 // [2 * grid][N][2]
   float* ws_acc;                // [2 * grid][N][D]
@@ -176,6 +181,16 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {  // the same value in every lane, and known to be
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle: K-major operands step
 // 1024 bytes per 8 rows (sbo); MN-major ones 1024 bytes per 8 k (sbo) and one
 // panel per 64 rows or columns (lbo).
@@ -187,6 +202,45 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 __host__ __device__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+__device__ __forceinline__ float warp_max(float x) {  // NaN counts only where all are
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 
 template <int C>
@@ -265,6 +319,13 @@ __device__ __forceinline__ void wht(float (&v)[NB][4], int lane) {
 
 // ------------------------------------------------------------------ split --
 
+// a / b for 0 <= a, 0 < b: 32-bit where both fit (a 64-bit division is a long
+// subroutine, and several stand in a launch's critical path)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // The flattened tiles [0, T) are cut into `parts` ranges of equal size.
 struct Cut {
   const int* prefix;  // tiles before each batch entry
@@ -274,7 +335,9 @@ struct Cut {
     total = (long long)pre[b] * units;
     parts = min((long long)grid, total);
   }
-  __device__ long long start(long long c) const { return c >= parts ? total : c * total / parts; }
+  __device__ long long start(long long c) const { return c >= parts ? total : quotient(c * total, parts); }
+  // the part that holds tile x
+  __device__ long long part_of(long long x) const { return quotient((x + 1) * parts - 1, total); }
 };
 
 struct Seg {
@@ -292,7 +355,7 @@ __device__ __forceinline__ Seg find(const Cut& cut, long long x, long long end, 
   s.b = lo;
   s.nt = cut.prefix[lo + 1] - cut.prefix[lo];
   const long long first = (long long)cut.prefix[lo] * cut.ub;
-  s.r = (int)((x - first) / s.nt);
+  s.r = (int)quotient(x - first, s.nt);
   s.kvh = s.r / n_hg;
   s.hg = s.r % n_hg;
   s.begin = first + (long long)s.r * s.nt;
@@ -370,9 +433,10 @@ __device__ __forceinline__ int clamp_nodes(const TreeParams& p, int b) {
   return p.n_nodes ? min(max(__ldg(p.n_nodes + b), 0), p.n_q) : p.n_q;
 }
 // The output row of column n of a row group, or -1.
-__device__ __forceinline__ long long out_row(const TreeParams& p, int b, int kvh, int vl, int nodes) {
-  const int G = p.q_heads / p.kv_heads;
-  const int j = vl / G;
+__device__ __forceinline__ long long out_row(const Params& P, int b, int kvh, int vl, int nodes) {
+  const TreeParams& p = P.t;
+  const int G = (int)P.group.d;
+  const int j = (int)P.group.div((uint32_t)vl);
   if (j >= nodes) return -1;
   return ((long long)b * p.n_q + j) * p.q_heads + kvh * G + (vl - j * G);
 }
@@ -514,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
+    regs_inc<kRegsSoft>();
     const int quad = warp & 3, grp = warp >> 2, tk = 32 * quad + lane;
     const int c0 = grp * HC;  // first column of this group
     const uint32_t tm_lane = (uint32_t)(32 * quad) << 16;
@@ -522,33 +587,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     float* red = miscf + M::kRed;  // [quad][N]
     const int gid = 2 + grp;       // named barrier of the group
     uint32_t tile_no = 0, seg_no = 0;  // across segments
-    const int G = p.q_heads / p.kv_heads;
+    const int rows = (int)P.group.d * p.n_q;  // of a kv-head
     for (long long x = begin; x < end; ++seg_no) {
       const Seg sg = find(cut, x, end, P.n_hg);
       const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
       const int nodes = clamp_nodes(p, sg.b), ctx = len - nodes;
       const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
-      // ---- the unit's rows: q^ = H (s o q), one power-of-two scale for all,
-      // split into two fp16 terms; column masks
+      // ---- the unit's rows: q^ = H (s o q), one power-of-two scale for all
+      // (|q^| <= 128 max |q|), split into two fp16 terms; column masks.  The
+      // loops stay rolled: this code runs once per unit, and fetching it cold
+      // would cost more than it saves (unrolled, 8 us for 64 rows).
       named_sync(1, 32 * kSoftWarps);  // both groups are done with the unit before
       float mul;
       {
-        constexpr int RW = N / kSoftWarps;  // rows per warp
-        float v[RW][NB][4];
-        const uint32_t sgn = p.sign_mask[lane >> 3] >> (4 * (lane & 7));
-        float mx = 0.0f;
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-          const int n = warp + kSoftWarps * i, vl = sg.hg * N + n;
-          const long long row = vl < G * p.n_q ? out_row(p, sg.b, sg.kvh, vl, nodes) : -1;
+        auto load_row = [&](int n, float (&v)[NB][4]) {
+          const int vl = sg.hg * N + n;
+          const long long row = vl < rows ? out_row(P, sg.b, sg.kvh, vl, nodes) : -1;
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk) {
-            v[i][blk][0] = v[i][blk][1] = v[i][blk][2] = v[i][blk][3] = 0.0f;
+            v[blk][0] = v[blk][1] = v[blk][2] = v[blk][3] = 0.0f;
             if (row >= 0) {
               const size_t e = (size_t)row * D + blk * kBlock + 4 * lane;
               if (p.q_dtype == TQ_F32) {
                 const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
-                v[i][blk][0] = a.x; v[i][blk][1] = a.y; v[i][blk][2] = a.z; v[i][blk][3] = a.w;
+                v[blk][0] = a.x; v[blk][1] = a.y; v[blk][2] = a.z; v[blk][3] = a.w;
               } else {
                 const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + e);
                 float2 a, c;
@@ -559,28 +621,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                   a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.x));
                   c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.y));
                 }
-                v[i][blk][0] = a.x; v[i][blk][1] = a.y; v[i][blk][2] = c.x; v[i][blk][3] = c.y;
+                v[blk][0] = a.x; v[blk][1] = a.y; v[blk][2] = c.x; v[blk][3] = c.y;
               }
             }
           }
-          if (lane == 0)
-            *reinterpret_cast<uint64_t*>(misc + M::kMask + 2 * n) =
-                row >= 0 ? __ldg(reinterpret_cast<const unsigned long long*>(p.tree) + (size_t)sg.b * p.n_q + vl / G) : 0ull;
+        };
+        if (tid < N) {
+          const int vl = sg.hg * N + tid;
+          const int j = (int)P.group.div((uint32_t)vl);
+          uint64_t w = 0;
+          if (vl < rows && j < nodes)
+            w = __ldg(reinterpret_cast<const unsigned long long*>(p.tree) + (size_t)sg.b * p.n_q + j);
+          *reinterpret_cast<uint64_t*>(misc + M::kMask + 2 * tid) = w;
         }
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if ((sgn >> k) & 1u) v[i][blk][k] = -v[i][blk][k];
-          wht<NB>(v[i], lane);
+        float mx = 0.0f;
+#pragma unroll 2
+        for (int n = warp; n < N; n += kSoftWarps) {
+          float v[NB][4];
+          load_row(n, v);
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float a = fabsf(v[i][blk][k]);
-              mx = fmaxf(mx, a < INFINITY ? a : 0.0f);  // rows that are not finite have no say
+              const float a = fabsf(v[blk][k]);
+              mx = fmaxf(mx, a < INFINITY ? a : 0.0f);  // elements that are not finite have no say
             }
         }
 #pragma unroll
@@ -589,21 +653,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         named_sync(1, 32 * kSoftWarps);
 #pragma unroll
         for (int w = 0; w < kSoftWarps; ++w) mx = fmaxf(mx, miscf[M::kQmax + w]);
-        const int qe = mx > 0.0f ? max(ilogbf(mx) - 13, -110) : 0;
+        // 128 max |q| scaled to below 2^15
+        const int qe = mx > 0.0f ? max(ilogbf(mx) - 7, -110) : 0;
         const float sc = ldexpf(1.0f, -qe);
         mul = p.score_mult * ldexpf(1.0f, qe) / P.kscale;
-        // lane l holds dims 4l..4l+3: chunk l / 2 of the block, half l & 1
+        const uint32_t sgn = p.sign_mask[lane >> 3] >> (4 * (lane & 7));
+#pragma unroll 2
+        for (int n = warp; n < N; n += kSoftWarps) {
+          float v[NB][4];
+          load_row(n, v);
 #pragma unroll
-        for (int i = 0; i < RW; ++i) {
-          const int n = warp + kSoftWarps * i;
+          for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[blk][k] *= ((sgn >> k) & 1u) ? -sc : sc;
+          wht<NB>(v, lane);
+          // lane l holds dims 4l..4l+3: chunk l / 2 of the block, half l & 1
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk) {
             const uint32_t a = pl.q + (uint32_t)(2 * blk + (lane >> 4)) * kQPanel + (uint32_t)n * 128u +
                                (uint32_t)((((lane >> 1) & 7) ^ (n & 7)) << 4) + 8u * (lane & 1);
-            float y[4];
+            const float(&y)[4] = v[blk];
             __half2 h[2], r[2];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = v[i][blk][k] * sc;
             h[0] = __floats2half2_rn(y[0], y[1]);
             h[1] = __floats2half2_rn(y[2], y[3]);
             const float2 b0 = __half22float2(h[0]), b1 = __half22float2(h[1]);
@@ -617,126 +687,139 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         __syncwarp();
         if (lane == 0) bar_arrive(bar(kQFull));
       }
-      if (tk < HC) miscf[M::kMoff + c0 + tk] = kUnset;
+      if (tk < HC) miscf[M::kMoff + c0 + tk] = -kUnset;  // the references are kept negated
       named_sync(gid, 128);
-      float l[HC];
+      float2 l[HC / 2];
 #pragma unroll
-      for (int c = 0; c < HC; ++c) l[c] = 0.0f;
+      for (int c = 0; c < HC / 2; ++c) l[c] = make_float2(0.0f, 0.0f);
       float vpow = 1.0f;  // 2^-e of the V norms, e the unit's scale
-      // this thread's norms of the next tile
-      float kn[NB], vn[NB];
+      // this thread's norms of the next tile, as they come from memory
+      uint16_t kn[NB], vn[NB];
       auto load_norms = [&](int tile) {
         const int t = tile * kTok + tk;
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          kn[blk] = vn[blk] = 0.0f;
+          kn[blk] = vn[blk] = 0;
           if (t < len) {
-            kn[blk] = __half2float(__ushort_as_half(__ldg(p.k_norms + (row0 + t) * NB + blk)));
-            vn[blk] = __half2float(__ushort_as_half(__ldg(p.v_norms + (row0 + t) * NB + blk)));
+            kn[blk] = __ldg(p.k_norms + (row0 + t) * NB + blk);
+            vn[blk] = __ldg(p.v_norms + (row0 + t) * NB + blk);
           }
         }
       };
       load_norms(sg.lo);
       for (int tile = sg.lo; tile < sg.hi; ++tile, ++tile_no) {
         const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
-        float f[NB], v_n[NB];
+        float f[NB], vs[NB], vbig = 0.0f;
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          f[blk] = kn[blk] * mul;
-          v_n[blk] = vn[blk];
+          f[blk] = __half2float(__ushort_as_half(kn[blk])) * mul;
+          vs[blk] = __half2float(__ushort_as_half(vn[blk]));
+          vbig = fmaxf(vbig, vs[blk] < INFINITY ? vs[blk] : 0.0f);
         }
         if (tile + 1 < sg.hi) load_norms(tile + 1);
         const int t = tile * kTok + tk, node = t - ctx;
         const bool masked = (tile + 1) * kTok > ctx;  // the tile holds drafted nodes or the end
         const uint32_t tm_s = tmem + tm_lane + st * (NB * N) + c0;
+        bool grown = false;  // the V scale changed in this tile
+        float beta = 1.0f;
         wait(kSFull + st, ph);
         tc_after();
-        // score of column c of the chunk, against no reference
-        auto load_scores = [&](int ch, float (&s)[CH]) {
-          tm_load<CH>(tm_s + ch * CH, s);
-          if constexpr (NB == 2) {
-            float s1[CH];
-            tm_load<CH>(tm_s + N + ch * CH, s1);
-            tc_wait_ld();
-#pragma unroll
-            for (int c = 0; c < CH; ++c) s[c] = fmaf(s1[c], f[NB - 1], s[c] * f[0]);
-          } else {
-            tc_wait_ld();
-#pragma unroll
-            for (int c = 0; c < CH; ++c) s[c] *= f[0];
-          }
-        };
-        auto sees = [&](int c) {  // does row c0 + c see this thread's position
-          uint64_t w;
-          asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(mask_a + 8u * c));
-          return t < len && (node < 0 || ((w >> node) & 1ull));
-        };
-        float top = -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < HC / CH; ++ch) {
-          float s[CH];
-          load_scores(ch, s);
+          float x[CH];         // scores against the references
+          uint32_t hidden = 0; // columns whose row does not see this position
           if (masked) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-              if (!sees(ch * CH + c)) s[c] = -INFINITY;
+            for (int c = 0; c < CH; ++c) {
+              uint64_t w;
+              asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(mask_a + 8u * (ch * CH + c)));
+              if (!(t < len && (node < 0 || ((w >> node) & 1ull)))) hidden |= 1u << c;
+            }
           }
+          auto load_scores = [&]() {
+            tm_load<CH>(tm_s + ch * CH, x);
+            if constexpr (NB == 2) {
+              float y[CH];
+              tm_load<CH>(tm_s + N + ch * CH, y);
+              tc_wait_ld();
 #pragma unroll
-          for (int c = 0; c < CH; c += 4) {
-            const float4 m = lds128f(moff_a + 4u * (ch * CH + c));
-            top = fmaxf(top, fmaxf(fmaxf(s[c] - m.x, s[c + 1] - m.y), fmaxf(s[c + 2] - m.z, s[c + 3] - m.w)));
-          }
-        }
-        float vbig = 0.0f;
+              for (int c = 0; c < CH; c += 2) {
+                const float2 r = fma2(make_float2(y[c], y[c + 1]), make_float2(f[NB - 1], f[NB - 1]),
+                                      mul2(make_float2(x[c], x[c + 1]), make_float2(f[0], f[0])));
+                x[c] = r.x;
+                x[c + 1] = r.y;
+              }
+            } else {
+              tc_wait_ld();
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk) vbig = fmaxf(vbig, v_n[blk] < INFINITY ? v_n[blk] : 0.0f);
-        const bool need = top > kTau || vbig * vpow > kNormRoom;
-        if (named_or(gid, 128, need)) {
-          // ---- new reference maxima and V scale: maxima of the tile per row
+              for (int c = 0; c < CH; c += 2) {
+                const float2 r = mul2(make_float2(x[c], x[c + 1]), make_float2(f[0], f[0]));
+                x[c] = r.x;
+                x[c + 1] = r.y;
+              }
+            }
+            if (masked) {
 #pragma unroll
-          for (int ch = 0; ch < HC / CH; ++ch) {
-            float s[CH];
-            load_scores(ch, s);
+              for (int c = 0; c < CH; ++c)
+                if ((hidden >> c) & 1u) x[c] = -INFINITY;
+            }
+          };
+          // rounded product first, then the difference: the maximum itself gives exactly 0
+          auto against = [&]() {
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < CH; c += 4) {
+              const float4 m = lds128f(moff_a + 4u * (ch * CH + c));
+              const float2 u = add2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
+              const float2 w = add2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
+              x[c] = u.x; x[c + 1] = u.y; x[c + 2] = w.x; x[c + 3] = w.y;
+              top = fmaxf(top, fmaxf(fmaxf(u.x, u.y), fmaxf(w.x, w.y)));
+            }
+            return top;
+          };
+          load_scores();
+          const float top = against();
+          const bool wide = ch == 0 ? vbig * vpow > kNormRoom : grown;
+          if (named_or(gid, 128, top > kTau || wide)) {
+            // ---- new references (and V scale): the tile's maximum of each row
+            load_scores();
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-              float y = s[c];
-              if (masked && !sees(ch * CH + c)) y = -INFINITY;
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+              const float y = warp_max(x[c]);
               if (lane == 0) red[quad * N + c0 + ch * CH + c] = y;
             }
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) vbig = fmaxf(vbig, __shfl_xor_sync(0xffffffffu, vbig, o));
-          if (lane == 0) miscf[M::kVmax + warp] = vbig;
-          named_sync(gid, 128);
-          if (tk < HC) {
-            const int c = c0 + tk;
-            const float y = fmaxf(fmaxf(red[c], red[N + c]), fmaxf(red[2 * N + c], red[3 * N + c]));
-            const float old = miscf[M::kMoff + c];
-            float a = 1.0f;
-            if (y > old + kTau) {
-              a = old == kUnset ? 0.0f : ex2(old - y);
-              miscf[M::kMoff + c] = y;
+            if (ch == 0) {
+              const float y = warp_max(vbig);
+              if (lane == 0) miscf[M::kVmax + warp] = y;
             }
-            miscf[M::kAlpha + c] = a;
-          }
-          float vm = 0.0f;
+            named_sync(gid, 128);
+            if (tk < CH) {
+              const int c = c0 + ch * CH + tk;
+              const float y = fmaxf(fmaxf(red[c], red[N + c]), fmaxf(red[2 * N + c], red[3 * N + c]));
+              const float old = -miscf[M::kMoff + c];
+              float a = 1.0f;
+              if (y > old + kTau) {
+                a = old == kUnset ? 0.0f : ex2(old - y);
+                miscf[M::kMoff + c] = -y;
+              }
+              miscf[M::kAlpha + c] = a;
+            }
+            if (ch == 0) {
+              float vm = 0.0f;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) vm = fmaxf(vm, miscf[M::kVmax + 4 * grp + w]);
-          float beta = 1.0f;
-          if (vm > 0.0f && (tile == sg.lo || vm * vpow > kNormRoom)) {
-            const float np = ldexpf(1.0f, -ilogbf(vm));
-            beta = np / vpow;
-            vpow = np;
-          }
-          named_sync(gid, 128);
-          if (tile > sg.lo) {
-            wait(kPFree, (tile_no - 1) & 1);  // the sum so far
-            tc_after();
-          }
-#pragma unroll
-          for (int ch = 0; ch < HC / CH; ++ch) {
+              for (int w = 0; w < 4; ++w) vm = fmaxf(vm, miscf[M::kVmax + 4 * grp + w]);
+              if (vm > 0.0f && (tile == sg.lo || vm * vpow > kNormRoom)) {
+                const float np = ldexpf(1.0f, -ilogbf(vm));
+                beta = np / vpow;
+                vpow = np;
+                grown = true;
+              }
+            }
+            named_sync(gid, 128);
+            if (tile > sg.lo) {
+              wait(kPFree, (tile_no - 1) & 1);  // the sum so far
+              tc_after();
+            }
             float a[CH];
 #pragma unroll
             for (int c = 0; c < CH; c += 4) {
@@ -744,7 +827,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               a[c] = m.x; a[c + 1] = m.y; a[c + 2] = m.z; a[c + 3] = m.w;
             }
 #pragma unroll
-            for (int c = 0; c < CH; ++c) l[ch * CH + c] *= a[c];
+            for (int c = 0; c < CH; c += 2) {
+              float2& y = l[(ch * CH + c) / 2];
+              y = mul2(y, make_float2(a[c], a[c + 1]));
+            }
             if (tile > sg.lo) {
 #pragma unroll
               for (int blk = 0; blk < NB; ++blk) {
@@ -755,35 +841,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 for (int c = 0; c < CH; ++c) o[c] *= a[c] * beta;
                 tm_store<CH>(tm_o + tm_lane + blk * N + c0 + ch * CH, o);
               }
+              tc_wait_st();
             }
+            load_scores();
+            against();
           }
-          tc_wait_st();
-        }
-        // ---- weights, their sums, and weight * norm as the MMA's operand
-        float vs[NB];
+          // ---- weights, their sums, and weight * norm as the MMA's operand
+          if (ch == 0) {
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk) vs[blk] = v_n[blk] * vpow;
-        if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);
-#pragma unroll
-        for (int ch = 0; ch < HC / CH; ++ch) {
-          float s[CH];
-          load_scores(ch, s);
-          uint32_t hidden = 0;
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-              if (!sees(ch * CH + c)) hidden |= 1u << c;
+            for (int blk = 0; blk < NB; ++blk) vs[blk] *= vpow;
+            if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);
+          }
+          if (ch == HC / CH - 1) {  // the scores are in registers
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(kSEmpty + st));
           }
 #pragma unroll
           for (int c = 0; c < CH; c += 8) {
-            const float4 m0 = lds128f(moff_a + 4u * (ch * CH + c)), m1 = lds128f(moff_a + 4u * (ch * CH + c + 4));
-            const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-            float w[8];
+            float2 w[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              w[k] = ex2(s[c + k] - m[k]);
-              if (masked && ((hidden >> (c + k)) & 1u)) w[k] = 0.0f;
-              l[ch * CH + c + k] += w[k];
+            for (int k = 0; k < 4; ++k) {
+              w[k] = make_float2(ex2(x[c + 2 * k]), ex2(x[c + 2 * k + 1]));
+              float2& y = l[(ch * CH + c) / 2 + k];
+              y = add2(y, w[k]);
             }
             const int col = c0 + ch * CH + c;
 #pragma unroll
@@ -791,12 +872,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               uint32_t h[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                float a = w[2 * k] * vs[blk], b = w[2 * k + 1] * vs[blk];
+                float2 y = mul2(w[k], make_float2(vs[blk], vs[blk]));
                 if (masked) {  // a hidden position's norm may be anything
-                  if ((hidden >> (c + 2 * k)) & 1u) a = 0.0f;
-                  if ((hidden >> (c + 2 * k + 1)) & 1u) b = 0.0f;
+                  if ((hidden >> (c + 2 * k)) & 1u) y.x = 0.0f;
+                  if ((hidden >> (c + 2 * k + 1)) & 1u) y.y = 0.0f;
                 }
-                const __half2 hh = __floats2half2_rn(a, b);
+                const __half2 hh = __floats2half2_rn(y.x, y.y);
                 h[k] = *reinterpret_cast<const uint32_t*>(&hh);
               }
               sts128(pl.pt + (uint32_t)(blk * ((N + 63) / 64) + (col >> 6)) * kPanel + (uint32_t)tk * 128u +
@@ -808,17 +889,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tc_before();
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          bar_arrive(bar(kSEmpty + st));
-          bar_arrive(bar(kPFull));
-        }
+        if (lane == 0) bar_arrive(bar(kPFull));
       }
       // ---- the segment's partial: l over the positions, O, reference maxima
       wait(kPFree, (tile_no - 1) & 1);
       tc_after();
 #pragma unroll
       for (int c = 0; c < HC; ++c) {
-        float y = l[c];
+        float y = c & 1 ? l[c / 2].y : l[c / 2].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (lane == 0) red[quad * N + c0 + c] = y;
@@ -829,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       float* acc = P.ws_acc + slot * N * D;
       if (tk < HC) {
         const int c = c0 + tk;
-        const float m = miscf[M::kMoff + c], sum = red[c] + red[N + c] + red[2 * N + c] + red[3 * N + c];
+        const float m = -miscf[M::kMoff + c], sum = red[c] + red[N + c] + red[2 * N + c] + red[3 * N + c];
         // a row with a NaN score keeps it through the join: its maximum is made infinite
         *reinterpret_cast<float2*>(ml + 2 * c) = make_float2(sum != sum ? INFINITY : m == kUnset ? -INFINITY : m, sum);
       }
@@ -849,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         named_sync(1, 32 * kSoftWarps);
         for (int n = warp; n < N; n += kSoftWarps) {
           const int vl = sg.hg * N + n;
-          const long long row = vl < G * p.n_q ? out_row(p, sg.b, sg.kvh, vl, nodes) : -1;
+          const long long row = vl < rows ? out_row(P, sg.b, sg.kvh, vl, nodes) : -1;
           if (row < 0) continue;
           float v[NB][4];
 #pragma unroll
@@ -864,6 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
   } else if (warp < 16) {
     // ============================================================ dequantise
+    regs_dec<kRegsCodes>();
     const int dq = warp - 8, side = dq >> 2, quarter = dq & 3;
     const uint32_t ring = pl.ring[dq];
     auto work = [&](auto bits_tag) {
@@ -924,66 +1003,86 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     else work(std::integral_constant<int, 4>{});
   } else {
     // ================================================================= MMAs
-    constexpr uint32_t id_s = mma_desc(N, false, false), id_o = mma_desc(N, true, true);
-    uint32_t ks = 0, kph = 0, vs = 0, vph = 0, tile_no = 0, seg_no = 0;
-    const bool one = lane == 0;
-    auto pv = [&](uint32_t no, bool first) {
-      wait(kPFull, no & 1);
-      tc_after();
-      for (int blk = 0; blk < NB; ++blk) {
-        wait(kVFull + vs, vph);
-        tc_after();
-        if (one) {
-          const uint32_t a = pl.vt + vs * 2 * kPanel, b = pl.pt + (uint32_t)(blk * ((N + 63) / 64)) * kPanel;
+    // Warp 16 issues the score products, warp 17 the V sums.  Descriptors and
+    // loop bounds are warp-uniform, so that they stay in uniform registers: an
+    // MMA of these shapes takes 32 to 64 cycles, and moving its descriptors
+    // into place must not take longer.
+    regs_dec<kRegsMma>();
+    if (warp == 16) {
+      constexpr uint32_t id_s = mma_desc(N, false, false);
+      uint32_t ks = 0, kph = 0, tile_no = 0, seg_no = 0;
+      const uint64_t dk = smem_desc(pl.kt, 16, 1024), dq = smem_desc(pl.q, 16, 1024);
+      const uint32_t tm = uniform(tmem);
+      for (long long x = begin; x < end; ++seg_no) {
+        const Seg sg = find(cut, x, end, P.n_hg);
+        const int tiles = uniform(sg.hi - sg.lo);
+        wait(kQFull, seg_no & 1);
+        for (int i = 0; i < tiles; ++i, ++tile_no) {
+          const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
+          wait(kSEmpty + st, ph ^ 1);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma(tm_o + blk * N, smem_desc(a + 2048u * k, kPanel, 1024), smem_desc(b + 2048u * k, kPanel, 1024), id_o,
-                   first && k == 0 ? 0u : 1u);
-          tc_commit(bar(kVEmpty + vs));
-          if (blk == NB - 1) tc_commit(bar(kPFree));
-        }
-        __syncwarp();
-        if (++vs == (uint32_t)pl.v_stages) {
-          vs = 0;
-          vph ^= 1;
-        }
-      }
-    };
-    for (long long x = begin; x < end; ++seg_no) {
-      const Seg sg = find(cut, x, end, P.n_hg);
-      wait(kQFull, seg_no & 1);
-      for (int tile = sg.lo; tile < sg.hi; ++tile, ++tile_no) {
-        const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
-        wait(kSEmpty + st, ph ^ 1);
-        tc_after();
-        for (int blk = 0; blk < NB; ++blk) {
-          wait(kKFull + ks, kph);
-          tc_after();
-          if (one) {
-            const uint32_t a = pl.kt + ks * 2 * kPanel;
+          for (int blk = 0; blk < NB; ++blk) {
+            wait(kKFull + ks, kph);
+            tc_after();
+            if (elect_one()) {
+              const uint64_t a = dk + (ks * 2 * kPanel >> 4), b = dq + (2 * blk * kQPanel >> 4);
+              const uint32_t d = tm + st * (NB * N) + blk * N;
 #pragma unroll
-            for (int half = 0; half < 2; ++half)  // the two terms of the query
+              for (int half = 0; half < 2; ++half)  // the two terms of the query
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t b = pl.q + (uint32_t)(half * 2 * NB + 2 * blk + (k >> 2)) * kQPanel + 32u * (k & 3);
-                tc_mma(tmem + st * (NB * N) + blk * N, smem_desc(a + (uint32_t)(k >> 2) * kPanel + 32u * (k & 3), 16, 1024),
-                       smem_desc(b, 16, 1024), id_s, half == 0 && k == 0 ? 0u : 1u);
-              }
-            tc_commit(bar(kKEmpty + ks));
-            if (blk == NB - 1) tc_commit(bar(kSFull + st));
-          }
-          __syncwarp();
-          if (++ks == (uint32_t)pl.k_stages) {
-            ks = 0;
-            kph ^= 1;
+                for (int k = 0; k < 8; ++k)
+                  tc_mma(d, a + (((k >> 2) * kPanel + 32u * (k & 3)) >> 4),
+                         b + (((half * 2 * NB + (k >> 2)) * kQPanel + 32u * (k & 3)) >> 4), id_s,
+                         half == 0 && k == 0 ? 0u : 1u);
+              tc_commit(bar(kKEmpty + ks));
+              if (blk == NB - 1) tc_commit(bar(kSFull + st));
+            }
+            __syncwarp();
+            if (++ks == (uint32_t)pl.k_stages) {
+              ks = 0;
+              kph ^= 1;
+            }
           }
         }
-        if (tile > sg.lo) pv(tile_no - 1, tile - 1 == sg.lo);
+        x = sg.begin + sg.hi;
       }
-      pv(tile_no - 1, sg.hi - 1 == sg.lo);
-      x = sg.begin + sg.hi;
+    } else if (warp == 17) {
+      constexpr uint32_t id_o = mma_desc(N, true, true);
+      constexpr uint32_t kPBlock = (uint32_t)((N + 63) / 64) * kPanel;
+      uint32_t vs = 0, vph = 0, tile_no = 0;
+      const uint64_t dv = smem_desc(pl.vt, kPanel, 1024), dp = smem_desc(pl.pt, kPanel, 1024);
+      const uint32_t to = uniform(tm_o);
+      for (long long x = begin; x < end;) {
+        const Seg sg = find(cut, x, end, P.n_hg);
+        const int tiles = uniform(sg.hi - sg.lo);
+        for (int i = 0; i < tiles; ++i, ++tile_no) {
+          wait(kPFull, tile_no & 1);
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            wait(kVFull + vs, vph);
+            tc_after();
+            if (elect_one()) {
+              const uint64_t a = dv + (vs * 2 * kPanel >> 4), b = dp + (blk * kPBlock >> 4);
+              const uint32_t d = to + blk * N;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc_mma(d, a + (2048u * k >> 4), b + (2048u * k >> 4), id_o, k == 0 ? (i > 0 ? 1u : 0u) : 1u);
+              tc_commit(bar(kVEmpty + vs));
+              if (blk == NB - 1) tc_commit(bar(kPFree));
+            }
+            __syncwarp();
+            if (++vs == (uint32_t)pl.v_stages) {
+              vs = 0;
+              vph ^= 1;
+            }
+          }
+        }
+        x = sg.begin + sg.hi;
+      }
+      // nothing is in flight when tensor memory is freed (every S product was
+      // waited for by the softmax warps)
+      if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);
     }
-    if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);  // nothing in flight when tensor memory is freed
   }
 
   tc_before();
@@ -1016,15 +1115,14 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Para
   if (c >= cut.parts) return;
   const long long x = cut.start(c);
   const Seg sg = find(cut, x, cut.total, P.n_hg);
-  if (sg.lo == 0 || cut.start(c - 1) > sg.begin) return;
+  if (sg.lo == 0 || cut.part_of(sg.begin) != c - 1) return;
   const int vl = sg.hg * N + n;
-  if (vl >= p.q_heads / p.kv_heads * p.n_q) return;
-  const long long row = out_row(p, sg.b, sg.kvh, vl, clamp_nodes(p, sg.b));
+  if (vl >= (int)P.group.d * p.n_q) return;
+  const long long row = out_row(P, sg.b, sg.kvh, vl, clamp_nodes(p, sg.b));
   if (row < 0) return;
   // part c - 1 holds the unit's first tiles (its last segment: slot 2 (c-1) + 1),
   // parts c, c + 1, ... the rest (their first segments: slots 2 c', ...)
-  long long last = c;
-  while (last + 1 < cut.parts && cut.start(last + 1) < sg.begin + sg.nt) ++last;
+  const long long last = cut.part_of(sg.begin + sg.nt - 1);
   const int parts = (int)(last - c) + 2;
   auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
   float top = -INFINITY, l = 0.0f;
@@ -1049,7 +1147,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Para
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[blk][k] *= down;
     const int m_parts = min(32, parts - i0);
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < m_parts; ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
       const float* acc = P.ws_acc + (slot(i0 + j) * N + n) * D + 4 * lane;
@@ -1166,6 +1264,7 @@ int run(Params& P, cudaStream_t stream) {
   const TreeParams& p = P.t;
   const int rows = p.q_heads / p.kv_heads * p.n_q;
   P.n_hg = (rows + N - 1) / N;
+  P.group = FastDiv::make((uint32_t)(p.q_heads / p.kv_heads));
   const long long tiles =
       (long long)p.batch * p.kv_heads * P.n_hg * ((p.seq_cap + kTok - 1) / kTok);
   int sms = 0;
@@ -1180,6 +1279,9 @@ int run(Params& P, cudaStream_t stream) {
   auto kern = tree_kernel<NB, N>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn) != cudaSuccess)
     return TQ_ERR_CUDA;
+  cudaFuncAttributes attr_k;
+  if (cudaFuncGetAttributes(&attr_k, kern) != cudaSuccess) return TQ_ERR_CUDA;
+  if (attr_k.numRegs < kRegsLaunch) return TQ_ERR_UNSUPPORTED;  // the register split would never be granted
   kern<<<grid, kThreads, P.pl.bytes, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
   if (grid == 1) return TQ_OK;  // no cut
