@@ -12,8 +12,10 @@
 //   O^T [128 dims x N rows]     += V^T [128 x 128] . P    per 128-block
 // Positions are the MMA's rows, so N adapts to the tree (16 to 128 columns), a
 // thread owns one position (its two norms are registers), and both operands
-// made from codes are written in the cache's own order: K^ as K-major rows,
-// V^ as M-major rows, P as N-major rows, 128-byte swizzled.
+// made from codes are written in the cache's own order: K^ as rows of tensor
+// memory, V^ as M-major and P as N-major rows of shared memory, 128-byte
+// swizzled.  Shared-memory bandwidth is what runs out first (table lookups, V^
+// and P in and out), so K^ does not pass through it.
 //
 // Softmax in the log2 domain with a lazy reference maximum per row: a tile is
 // scored against it, and only when some score exceeds it by 2^kTau do the
@@ -58,11 +60,11 @@ constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element x 128-row panel
 
 struct Plan {
   uint32_t bytes;
-  uint32_t q, kt, vt, pt;       // Q^ (hi, lo), K^ and V^ stages, P
+  uint32_t q, vt, pt;           // Q^ (hi, lo), V^ stages, P stages
   uint32_t lut_k, lut_v;
   uint32_t ring[8];             // code rings of the eight dequantising warps
   uint32_t bar, misc, prefix;
-  int k_stages, v_stages, depth;
+  int v_stages, p_stages, depth;
 };
 
 struct Params {
@@ -181,6 +183,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 
+// the same with A in tensor memory (lane: row, a column: two consecutive k)
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(r));
@@ -383,10 +393,9 @@ struct Slot {  // a ring slot: 32 positions, one block; padded so that 128-bit r
 };
 __host__ __device__ constexpr uint32_t slot_bytes(int bits) { return 32u * (bits == 4 ? 80u : 48u); }
 
-// The values of one position and block: 64 pairs, written as 16 chunks of 8 fp16.
+// The codes of one position and block.
 template <int B>
-__device__ __forceinline__ void expand_row(uint32_t slot_row, uint32_t dst_row, int tok, uint32_t lane_base) {
-  uint32_t w[4 * B];
+__device__ __forceinline__ void read_codes(uint32_t slot_row, uint32_t (&w)[4 * B]) {
 #pragma unroll
   for (int i = 0; i < B; ++i) {
     const uint4 x = lds128(slot_row + 16u * i);
@@ -395,6 +404,10 @@ __device__ __forceinline__ void expand_row(uint32_t slot_row, uint32_t dst_row, 
     w[4 * i + 2] = x.z;
     w[4 * i + 3] = x.w;
   }
+}
+// Their values as 16 chunks of 8 fp16, into the row of a swizzled tile.
+template <int B>
+__device__ __forceinline__ void expand_to_smem(const uint32_t (&w)[4 * B], uint32_t dst_row, int tok, uint32_t lane_base) {
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     uint32_t v[4];
@@ -402,6 +415,18 @@ __device__ __forceinline__ void expand_row(uint32_t slot_row, uint32_t dst_row, 
     for (int i = 0; i < 4; ++i) v[i] = lds_table(pair_addr<B>(w, 4 * c + i, lane_base));
     sts128(dst_row + (uint32_t)(c >> 3) * kPanel + (uint32_t)(((c & 7) ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
   }
+}
+// Their values as 64 columns of this lane's row of tensor memory.
+template <int B>
+__device__ __forceinline__ void expand_to_tmem(const uint32_t (&w)[4 * B], uint32_t addr, uint32_t lane_base) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(lds_table(pair_addr<B>(w, 16 * c + i, lane_base)));
+    tm_store<16>(addr + 16 * c, v);
+  }
+  tc_wait_st();
 }
 
 // ------------------------------------------------------------------ output --
@@ -443,7 +468,8 @@ __device__ __forceinline__ long long out_row(const Params& P, int b, int kvh, in
 
 // --------------------------------------------------------------- the kernel --
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 13, kQFull = 14, kBars = 15 };
+// barriers, two stages each but the last
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 14, kQFull = 16, kBars = 17 };
 
 // word offsets in the misc area
 template <int N>
@@ -463,9 +489,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   constexpr int D = NB * kBlock;
   constexpr int HC = N / 2;                 // rows (columns of S) of a softmax group
   constexpr int CH = HC < 32 ? HC : 32;     // columns per tensor-memory load
-  constexpr uint32_t kCols = 3 * NB * N <= 64 ? 64 : 3 * NB * N <= 128 ? 128 : 3 * NB * N <= 256 ? 256 : 512;
-  static_assert(3 * NB * N <= 512, "tensor memory");
+  // tensor memory: two stages of S, O, two stages of K^ (64 columns each)
+  constexpr uint32_t kColsO = 2 * NB * N, kColsK = 3 * NB * N, kColsUsed = 3 * NB * N + 128;
+  constexpr uint32_t kCols = kColsUsed <= 256 ? 256 : 512;
+  static_assert(kColsUsed <= 512, "tensor memory");
   constexpr uint32_t kQPanel = N * 128;     // bytes of a 64-dim panel of Q^
+  constexpr uint32_t kPBlock = (uint32_t)((N + 63) / 64) * kPanel, kPStage = NB * kPBlock;
   using M = Misc<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const TreeParams& p = P.t;
@@ -498,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       bar_init(bar(kVEmpty + s), 1);
       bar_init(bar(kSFull + s), 1);
       bar_init(bar(kSEmpty + s), kSoftWarps);
+      bar_init(bar(kPFull + s), kSoftWarps);
+      bar_init(bar(kPFree + s), 1);
     }
-    bar_init(bar(kPFull), kSoftWarps);
-    bar_init(bar(kPFree), 1);
     bar_init(bar(kQFull), kSoftWarps);
     misc[M::kAbort] = 0;
     misc[M::kAnyEmpty] = 0;
@@ -574,7 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const int ub = p.kv_heads * P.n_hg;
   const Cut cut(prefix, p.batch, ub, gridDim.x);
   const long long begin = cut.start(blockIdx.x), end = blockIdx.x < cut.parts ? cut.start(blockIdx.x + 1) : begin;
-  const uint32_t tm_o = tmem + 2 * NB * N;  // O columns follow the two S stages
+  const uint32_t tm_o = tmem + kColsO;
+  // P: tile n uses stage n mod p_stages (1 or 2)
+  const uint32_t p_shift = (uint32_t)pl.p_stages - 1;
+  auto p_stage = [&](uint32_t n) { return n & p_shift; };
+  auto p_phase = [&](uint32_t n) { return (n >> p_shift) & 1u; };
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
@@ -720,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const int t = tile * kTok + tk, node = t - ctx;
         const bool masked = (tile + 1) * kTok > ctx;  // the tile holds drafted nodes or the end
         const uint32_t tm_s = tmem + tm_lane + st * (NB * N) + c0;
+        const uint32_t pt = pl.pt + p_stage(tile_no) * kPStage;
         bool grown = false;  // the V scale changed in this tile
         float beta = 1.0f;
         wait(kSFull + st, ph);
@@ -817,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             named_sync(gid, 128);
             if (tile > sg.lo) {
-              wait(kPFree, (tile_no - 1) & 1);  // the sum so far
+              wait(kPFree + p_stage(tile_no - 1), p_phase(tile_no - 1));  // the sum so far
               tc_after();
             }
             float a[CH];
@@ -850,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (ch == 0) {
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) vs[blk] *= vpow;
-            if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);
+            wait(kPFree + p_stage(tile_no), p_phase(tile_no) ^ 1);
           }
           if (ch == HC / CH - 1) {  // the scores are in registers
             tc_before();
@@ -880,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 const __half2 hh = __floats2half2_rn(y.x, y.y);
                 h[k] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              sts128(pl.pt + (uint32_t)(blk * ((N + 63) / 64) + (col >> 6)) * kPanel + (uint32_t)tk * 128u +
+              sts128(pt + (uint32_t)(blk * ((N + 63) / 64) + (col >> 6)) * kPanel + (uint32_t)tk * 128u +
                          (uint32_t)((((col >> 3) & 7) ^ (tk & 7)) << 4),
                      h[0], h[1], h[2], h[3]);
             }
@@ -889,10 +923,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tc_before();
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) bar_arrive(bar(kPFull));
+        if (lane == 0) bar_arrive(bar(kPFull + p_stage(tile_no)));
       }
       // ---- the segment's partial: l over the positions, O, reference maxima
-      wait(kPFree, (tile_no - 1) & 1);
+      wait(kPFree + p_stage(tile_no - 1), p_phase(tile_no - 1));
       tc_after();
 #pragma unroll
       for (int c = 0; c < HC; ++c) {
@@ -951,8 +985,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       constexpr uint32_t kSlot = 32 * kStride;
       const uint8_t* codes = side ? p.v_codes : p.k_codes;
       const uint32_t lane_base = (side ? pl.lut_v : pl.lut_k) + 4u * lane;
-      const uint32_t stage0 = side ? pl.vt : pl.kt;
-      const int stages = side ? pl.v_stages : pl.k_stages, depth = pl.depth;
+      const uint32_t tm_k = tmem + ((uint32_t)(32 * quarter) << 16) + kColsK;
+      const int stages = side ? pl.v_stages : 2, depth = pl.depth;
       const int full = side ? kVFull : kKFull, emptyb = side ? kVEmpty : kKEmpty;
       const int tok = 32 * quarter + lane;
       uint32_t stage = 0, ephase = 1;  // the first round finds the stages free
@@ -980,11 +1014,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int item = 0; item < items; ++item) {
           cp_wait(depth - 1);
           __syncwarp();
-          wait(emptyb + stage, ephase);
-          const uint32_t dst = stage0 + stage * 2 * kPanel + (uint32_t)tok * 128u;
-          expand_row<B>(ring + (uint32_t)cslot * kSlot + (uint32_t)(lane * kStride), dst, tok, lane_base);
+          uint32_t w[4 * B];
+          read_codes<B>(ring + (uint32_t)cslot * kSlot + (uint32_t)(lane * kStride), w);
           if (++cslot == depth) cslot = 0;
-          fence_async_smem();
+          wait(emptyb + stage, ephase);
+          if (side) {
+            expand_to_smem<B>(w, pl.vt + stage * 2 * kPanel + (uint32_t)tok * 128u, tok, lane_base);
+            fence_async_smem();
+          } else {
+            tc_after();
+            expand_to_tmem<B>(w, tm_k + stage * 64, lane_base);
+            tc_before();
+          }
           __syncwarp();
           if (lane == 0) bar_arrive(bar(full + stage));
           issue(item + depth);
@@ -1011,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (warp == 16) {
       constexpr uint32_t id_s = mma_desc(N, false, false);
       uint32_t ks = 0, kph = 0, tile_no = 0, seg_no = 0;
-      const uint64_t dk = smem_desc(pl.kt, 16, 1024), dq = smem_desc(pl.q, 16, 1024);
+      const uint64_t dq = smem_desc(pl.q, 16, 1024);
       const uint32_t tm = uniform(tmem);
       for (long long x = begin; x < end; ++seg_no) {
         const Seg sg = find(cut, x, end, P.n_hg);
@@ -1025,30 +1066,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             wait(kKFull + ks, kph);
             tc_after();
             if (elect_one()) {
-              const uint64_t a = dk + (ks * 2 * kPanel >> 4), b = dq + (2 * blk * kQPanel >> 4);
+              const uint32_t a = tm + kColsK + ks * 64;
+              const uint64_t b = dq + (2 * blk * kQPanel >> 4);
               const uint32_t d = tm + st * (NB * N) + blk * N;
 #pragma unroll
               for (int half = 0; half < 2; ++half)  // the two terms of the query
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                  tc_mma(d, a + (((k >> 2) * kPanel + 32u * (k & 3)) >> 4),
+                  tc_mma_ta(d, a + 8 * k,
                          b + (((half * 2 * NB + (k >> 2)) * kQPanel + 32u * (k & 3)) >> 4), id_s,
                          half == 0 && k == 0 ? 0u : 1u);
               tc_commit(bar(kKEmpty + ks));
               if (blk == NB - 1) tc_commit(bar(kSFull + st));
             }
             __syncwarp();
-            if (++ks == (uint32_t)pl.k_stages) {
-              ks = 0;
-              kph ^= 1;
-            }
+            ks ^= 1;
+            kph ^= ks ^ 1;
           }
         }
         x = sg.begin + sg.hi;
       }
     } else if (warp == 17) {
       constexpr uint32_t id_o = mma_desc(N, true, true);
-      constexpr uint32_t kPBlock = (uint32_t)((N + 63) / 64) * kPanel;
       uint32_t vs = 0, vph = 0, tile_no = 0;
       const uint64_t dv = smem_desc(pl.vt, kPanel, 1024), dp = smem_desc(pl.pt, kPanel, 1024);
       const uint32_t to = uniform(tm_o);
@@ -1056,19 +1095,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const Seg sg = find(cut, x, end, P.n_hg);
         const int tiles = uniform(sg.hi - sg.lo);
         for (int i = 0; i < tiles; ++i, ++tile_no) {
-          wait(kPFull, tile_no & 1);
+          wait(kPFull + p_stage(tile_no), p_phase(tile_no));
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk) {
             wait(kVFull + vs, vph);
             tc_after();
             if (elect_one()) {
-              const uint64_t a = dv + (vs * 2 * kPanel >> 4), b = dp + (blk * kPBlock >> 4);
+              const uint64_t a = dv + (vs * 2 * kPanel >> 4);
+              const uint64_t b = dp + ((p_stage(tile_no) * kPStage + blk * kPBlock) >> 4);
               const uint32_t d = to + blk * N;
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 tc_mma(d, a + (2048u * k >> 4), b + (2048u * k >> 4), id_o, k == 0 ? (i > 0 ? 1u : 0u) : 1u);
               tc_commit(bar(kVEmpty + vs));
-              if (blk == NB - 1) tc_commit(bar(kPFree));
+              if (blk == NB - 1) tc_commit(bar(kPFree + p_stage(tile_no)));
             }
             __syncwarp();
             if (++vs == (uint32_t)pl.v_stages) {
@@ -1081,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       // nothing is in flight when tensor memory is freed (every S product was
       // waited for by the softmax warps)
-      if (tile_no > 0) wait(kPFree, (tile_no - 1) & 1);
+      if (tile_no > 0) wait(kPFree + p_stage(tile_no - 1), p_phase(tile_no - 1));
     }
   }
 
@@ -1220,8 +1260,8 @@ struct Place {
 
 template <int NB, int N>
 bool plan(const TreeParams& p, Plan& pl) {
-  // in order of preference: stages of K^ and V^, slots of a code ring
-  static const int tries[6][3] = {{2, 2, 3}, {2, 2, 2}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}};
+  // in order of preference: stages of V^ and P, slots of a code ring
+  static const int tries[5][3] = {{2, 2, 3}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}};
   for (const auto& t : tries) {
     pl = Plan{};
     Place at;
@@ -1233,15 +1273,14 @@ bool plan(const TreeParams& p, Plan& pl) {
       if (a + size > end) end = a + size;
       return a;
     };
-    pl.k_stages = t[0];
-    pl.v_stages = t[1];
+    pl.v_stages = t[0];
+    pl.p_stages = t[1];
     pl.depth = t[2];
     pl.lut_k = take(128u << (2 * p.k_bits), 128u << (2 * p.k_bits));
     pl.lut_v = take(128u << (2 * p.v_bits), 128u << (2 * p.v_bits));
-    pl.kt = take(2 * kPanel * t[0], 1024);
-    pl.vt = take(2 * kPanel * t[1], 1024);
+    pl.vt = take(2 * kPanel * t[0], 1024);
     pl.q = take((uint32_t)(4 * NB * N * 128), 1024);
-    pl.pt = take((uint32_t)(NB * ((N + 63) / 64)) * kPanel, 1024);
+    pl.pt = take((uint32_t)(t[1] * NB * ((N + 63) / 64)) * kPanel, 1024);
     for (int w = 0; w < 8; ++w) pl.ring[w] = take(slot_bytes(w < 4 ? p.k_bits : p.v_bits) * t[2], 128);
     pl.bar = take(8 * kBars, 128);
     pl.misc = take(4 * Misc<N>::kWords, 128);
