@@ -26,8 +26,7 @@
 // (two MMAs), the centroids are scaled by a factor that makes their rounding
 // small (centroid_scale), and weight * norm is rounded once.
 //
-// Warps: 0-7 softmax (two groups of 128 threads, half the rows each), 8-11 K
-// and 12-15 V from codes to fp16, 16 and 17 issue the MMAs (18 and 19 idle).
+// Warps: see Roles.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,13 +42,19 @@ namespace tree {
 namespace {
 
 constexpr int kTok = 128;           // positions per tile
-constexpr int kWarps = 20;          // five warpgroups, for the register split
-constexpr int kThreads = 32 * kWarps;
-// Registers per thread: at launch, then of the softmax (two warpgroups), the
-// dequantising (two) and the MMA warpgroup.  The shares must fit the launch's.
-constexpr int kRegsLaunch = 96, kRegsSoft = 136, kRegsCodes = 72, kRegsMma = 64;
-static_assert(2 * kRegsSoft + 2 * kRegsCodes + kRegsMma <= 5 * kRegsLaunch, "register split");
-constexpr int kSoftWarps = 8;
+// Roles by warpgroup (four warps): softmax groups of 128 threads, each with its
+// share of the row group's columns, then two that turn codes into fp16, then
+// one whose first two warps issue the MMAs.  Registers per thread at launch,
+// then by role: the shares must fit the launch's total.
+template <int N>
+struct Roles {
+  static constexpr int kGroups = N >= 64 ? 4 : 2;
+  static constexpr int kSoftWarps = 4 * kGroups, kCodeWarp = kSoftWarps, kMmaWarp = kSoftWarps + 8;
+  static constexpr int kWarps = kSoftWarps + 12, kThreads = 32 * kWarps;
+  static constexpr int kLaunch = kGroups == 4 ? 72 : 96;
+  static constexpr int kSoft = kGroups == 4 ? 80 : 136, kCodes = 72, kMma = kGroups == 4 ? 40 : 64;
+  static_assert(kGroups * kSoft + 2 * kCodes + kMma <= (kGroups + 3) * kLaunch, "register split");
+};
 constexpr int kMaxGrid = 256;       // CTAs at most (slots of the workspace)
 constexpr uint32_t kBase = 1024;    // shared-window address of dynamic shared memory
 constexpr uint32_t kMaxDyn = 227 * 1024;
@@ -112,11 +117,22 @@ __device__ __forceinline__ uint32_t lds_table(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ void sts16(uint32_t a, unsigned short x) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(x) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait(int pending) {
@@ -391,7 +407,10 @@ template <int B>
 struct Slot {  // a ring slot: 32 positions, one block; padded so that 128-bit reads of 8 lanes hit distinct banks
   static constexpr int kStride = B == 4 ? 80 : 48;
 };
-__host__ __device__ constexpr uint32_t slot_bytes(int bits) { return 32u * (bits == 4 ? 80u : 48u); }
+// K slots end with the positions' K norms and V norms, 64 bytes each per block.
+__host__ __device__ constexpr uint32_t slot_bytes(int bits, int norm_blocks) {
+  return 32u * (bits == 4 ? 80u : 48u) + 128u * (uint32_t)norm_blocks;
+}
 
 // The codes of one position and block.
 template <int B>
@@ -405,15 +424,16 @@ __device__ __forceinline__ void read_codes(uint32_t slot_row, uint32_t (&w)[4 * 
     w[4 * i + 3] = x.w;
   }
 }
-// Their values as 16 chunks of 8 fp16, into the row of a swizzled tile.
+// Their values as 16 chunks of 8 fp16, into the row of a swizzled tile whose
+// chunk 0 is at dst_row.
 template <int B>
-__device__ __forceinline__ void expand_to_smem(const uint32_t (&w)[4 * B], uint32_t dst_row, int tok, uint32_t lane_base) {
+__device__ __forceinline__ void expand_to_smem(const uint32_t (&w)[4 * B], uint32_t dst_row, uint32_t lane_base) {
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lds_table(pair_addr<B>(w, 4 * c + i, lane_base));
-    sts128(dst_row + (uint32_t)(c >> 3) * kPanel + (uint32_t)(((c & 7) ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
+    sts128((dst_row ^ (uint32_t)((c & 7) << 4)) + (uint32_t)(c >> 3) * kPanel, v[0], v[1], v[2], v[3]);
   }
 }
 // Their values as 64 columns of this lane's row of tensor memory.
@@ -472,30 +492,33 @@ __device__ __forceinline__ long long out_row(const Params& P, int b, int kvh, in
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 14, kQFull = 16, kBars = 17 };
 
 // word offsets in the misc area
-template <int N>
+template <int NB, int N>
 struct Misc {
-  static constexpr int kAbort = 0, kTmem = 1, kAnyEmpty = 2, kQmax = 4;      // [8]
-  static constexpr int kVmax = kQmax + 8;                                    // [8]
-  static constexpr int kMoff = kVmax + 8;                                    // [N]
+  static constexpr int kAbort = 0, kTmem = 1, kAnyEmpty = 2, kQmax = 4;      // [16]
+  static constexpr int kVmax = kQmax + 16;                                   // [16]
+  static constexpr int kMoff = kVmax + 16;                                   // [N]
   static constexpr int kAlpha = kMoff + N;                                   // [N]
   static constexpr int kRed = kAlpha + N;                                    // [4][N]
   static constexpr int kMask = kRed + 4 * N;                                 // [N] 64-bit
   static constexpr int kScan = kMask + 2 * N;                                // [16]
-  static constexpr int kWords = kScan + 16;
+  static constexpr int kNorm = kScan + 16;                                   // [4 tiles][block][K, V][128]
+  static constexpr int kWords = kNorm + 4 * NB * 2 * kTok;
 };
 
 template <int NB, int N>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __grid_constant__ Params P) {
   constexpr int D = NB * kBlock;
-  constexpr int HC = N / 2;                 // rows (columns of S) of a softmax group
-  constexpr int CH = HC < 32 ? HC : 32;     // columns per tensor-memory load
+  using Ro = Roles<N>;
+  constexpr int kGroups = Ro::kGroups, kSoftWarps = Ro::kSoftWarps, kThreads = Ro::kThreads;
+  constexpr int HC = N / kGroups;           // rows (columns of S) of a softmax group
+  constexpr int CH = HC < 16 ? HC : 16;     // columns per tensor-memory load
   // tensor memory: two stages of S, O, two stages of K^ (64 columns each)
   constexpr uint32_t kColsO = 2 * NB * N, kColsK = 3 * NB * N, kColsUsed = 3 * NB * N + 128;
   constexpr uint32_t kCols = kColsUsed <= 256 ? 256 : 512;
   static_assert(kColsUsed <= 512, "tensor memory");
   constexpr uint32_t kQPanel = N * 128;     // bytes of a 64-dim panel of Q^
   constexpr uint32_t kPBlock = (uint32_t)((N + 63) / 64) * kPanel, kPStage = NB * kPBlock;
-  using M = Misc<N>;
+  using M = Misc<NB, N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const TreeParams& p = P.t;
   const Plan& pl = P.pl;
@@ -535,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     misc[M::kAnyEmpty] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) {
+  if (warp == Ro::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(pl.misc + 4 * M::kTmem),
                  "r"(kCols)
                  : "memory");
@@ -611,10 +634,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
-    regs_inc<kRegsSoft>();
+    regs_inc<Ro::kSoft>();
     const int quad = warp & 3, grp = warp >> 2, tk = 32 * quad + lane;
     const int c0 = grp * HC;  // first column of this group
     const uint32_t tm_lane = (uint32_t)(32 * quad) << 16;
+    const uint32_t tk_row = (uint32_t)tk * 128u + (uint32_t)((tk & 7) << 4);  // P row, chunk 0
     const uint32_t moff_a = pl.misc + 4u * (M::kMoff + c0), alpha_a = pl.misc + 4u * (M::kAlpha + c0);
     const uint32_t mask_a = pl.misc + 4u * (M::kMask + 2 * c0);
     float* red = miscf + M::kRed;  // [quad][N]
@@ -625,7 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const Seg sg = find(cut, x, end, P.n_hg);
       const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
       const int nodes = clamp_nodes(p, sg.b), ctx = len - nodes;
-      const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
       // ---- the unit's rows: q^ = H (s o q), one power-of-two scale for all
       // (|q^| <= 128 max |q|), split into two fp16 terms; column masks.  The
       // loops stay rolled: this code runs once per unit, and fetching it cold
@@ -726,30 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
       for (int c = 0; c < HC / 2; ++c) l[c] = make_float2(0.0f, 0.0f);
       float vpow = 1.0f;  // 2^-e of the V norms, e the unit's scale
-      // this thread's norms of the next tile, as they come from memory
-      uint16_t kn[NB], vn[NB];
-      auto load_norms = [&](int tile) {
-        const int t = tile * kTok + tk;
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-          kn[blk] = vn[blk] = 0;
-          if (t < len) {
-            kn[blk] = __ldg(p.k_norms + (row0 + t) * NB + blk);
-            vn[blk] = __ldg(p.v_norms + (row0 + t) * NB + blk);
-          }
-        }
-      };
-      load_norms(sg.lo);
       for (int tile = sg.lo; tile < sg.hi; ++tile, ++tile_no) {
         const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
-        float f[NB], vs[NB], vbig = 0.0f;
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-          f[blk] = __half2float(__ushort_as_half(kn[blk])) * mul;
-          vs[blk] = __half2float(__ushort_as_half(vn[blk]));
-          vbig = fmaxf(vbig, vs[blk] < INFINITY ? vs[blk] : 0.0f);
-        }
-        if (tile + 1 < sg.hi) load_norms(tile + 1);
         const int t = tile * kTok + tk, node = t - ctx;
         const bool masked = (tile + 1) * kTok > ctx;  // the tile holds drafted nodes or the end
         const uint32_t tm_s = tmem + tm_lane + st * (NB * N) + c0;
@@ -758,18 +759,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         float beta = 1.0f;
         wait(kSFull + st, ph);
         tc_after();
+        // this position's norms, left there with its codes
+        float f[NB], vs[NB], vbig = 0.0f, vbig_all = 0.0f;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          const float* nrm = miscf + M::kNorm + ((tile_no & 3) * NB + blk) * 2 * kTok + tk;
+          f[blk] = nrm[0] * mul;
+          vs[blk] = nrm[kTok];
+          const float size = fabsf(vs[blk]);
+          vbig = fmaxf(vbig, size < INFINITY ? size : 0.0f);
+          vbig_all = size < INFINITY ? vbig_all : INFINITY;
+        }
 #pragma unroll
         for (int ch = 0; ch < HC / CH; ++ch) {
-          float x[CH];         // scores against the references
-          uint32_t hidden = 0; // columns whose row does not see this position
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              uint64_t w;
-              asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(mask_a + 8u * (ch * CH + c)));
-              if (!(t < len && (node < 0 || ((w >> node) & 1ull)))) hidden |= 1u << c;
-            }
-          }
+          float x[CH];  // scores, then scores against the references
+          auto sees = [&](int c) {  // whether column c's row sees this position
+            uint64_t w;
+            asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(mask_a + 8u * (ch * CH + c)));
+            return t < len && (node < 0 || ((w >> node) & 1ull));
+          };
           auto load_scores = [&]() {
             tm_load<CH>(tm_s + ch * CH, x);
             if constexpr (NB == 2) {
@@ -795,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (masked) {
 #pragma unroll
               for (int c = 0; c < CH; ++c)
-                if ((hidden >> c) & 1u) x[c] = -INFINITY;
+                if (!sees(c)) x[c] = -INFINITY;
             }
           };
           // rounded product first, then the difference: the maximum itself gives exactly 0
@@ -807,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               const float2 u = add2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
               const float2 w = add2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
               x[c] = u.x; x[c + 1] = u.y; x[c + 2] = w.x; x[c + 3] = w.y;
-              top = fmaxf(top, fmaxf(fmaxf(u.x, u.y), fmaxf(w.x, w.y)));
+              top = max3(max3(top, u.x, u.y), w.x, w.y);
             }
             return top;
           };
@@ -906,17 +914,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               uint32_t h[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                float2 y = mul2(w[k], make_float2(vs[blk], vs[blk]));
-                if (masked) {  // a hidden position's norm may be anything
-                  if ((hidden >> (c + 2 * k)) & 1u) y.x = 0.0f;
-                  if ((hidden >> (c + 2 * k + 1)) & 1u) y.y = 0.0f;
-                }
+                const float2 y = mul2(w[k], make_float2(vs[blk], vs[blk]));
                 const __half2 hh = __floats2half2_rn(y.x, y.y);
                 h[k] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-              sts128(pt + (uint32_t)(blk * ((N + 63) / 64) + (col >> 6)) * kPanel + (uint32_t)tk * 128u +
-                         (uint32_t)((((col >> 3) & 7) ^ (tk & 7)) << 4),
+              // column col's chunk of this position's row, swizzled
+              sts128(pt + (uint32_t)blk * kPBlock + (uint32_t)(col >> 6) * kPanel + (tk_row ^ (uint32_t)((col & 63) << 1)),
                      h[0], h[1], h[2], h[3]);
+            }
+          }
+          if (masked && !(vbig_all < INFINITY)) {
+            // an infinite or NaN norm times a weight of zero: rows that do not
+            // see the position get a plain zero
+#pragma unroll 1
+            for (int c = 0; c < CH; ++c) {
+              if (sees(c)) continue;
+              const int col = c0 + ch * CH + c;
+              for (int blk = 0; blk < NB; ++blk)
+                sts16(pt + (uint32_t)blk * kPBlock + (uint32_t)(col >> 6) * kPanel + (tk_row ^ (uint32_t)((col & 56) << 1)) +
+                          2u * (col & 7),
+                      0);
             }
           }
         }
@@ -974,21 +991,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       x = sg.begin + sg.hi;
     }
-  } else if (warp < 16) {
+  } else if (warp < Ro::kMmaWarp) {
     // ============================================================ dequantise
-    regs_dec<kRegsCodes>();
-    const int dq = warp - 8, side = dq >> 2, quarter = dq & 3;
+    if constexpr (Ro::kCodes < Ro::kLaunch) regs_dec<Ro::kCodes>();
+    const int dq = warp - Ro::kCodeWarp, side = dq >> 2, quarter = dq & 3;
     const uint32_t ring = pl.ring[dq];
     auto work = [&](auto bits_tag) {
       constexpr int B = decltype(bits_tag)::value;
       constexpr int kStride = Slot<B>::kStride;
-      constexpr uint32_t kSlot = 32 * kStride;
+      const uint32_t kSlot = slot_bytes(B, side ? 0 : NB);
       const uint8_t* codes = side ? p.v_codes : p.k_codes;
       const uint32_t lane_base = (side ? pl.lut_v : pl.lut_k) + 4u * lane;
       const uint32_t tm_k = tmem + ((uint32_t)(32 * quarter) << 16) + kColsK;
       const int stages = side ? pl.v_stages : 2, depth = pl.depth;
       const int full = side ? kVFull : kKFull, emptyb = side ? kVEmpty : kKEmpty;
       const int tok = 32 * quarter + lane;
+      uint32_t tile_no = 0;
       uint32_t stage = 0, ephase = 1;  // the first round finds the stages free
       int cslot = 0, islot = 0;
       for (long long x = begin; x < end;) {
@@ -1006,6 +1024,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               const uint8_t* src = codes + ((row0 + (ok ? t0 + tt : 0)) * NB + blk) * (16 * B) + 16 * part;
               cp_async16(ring + (uint32_t)islot * kSlot + (uint32_t)(tt * kStride + 16 * part), src, ok ? 16u : 0u);
             }
+            if (!side && blk == 0) {  // two norms per copy: 16 NB copies for K, then for V
+              const int left = (len - t0) * NB;  // norms from t0 to the end
+#pragma unroll
+              for (int r = 0; r < NB; ++r) {
+                const int c = lane + 32 * r, of_v = c / (16 * NB), i = c % (16 * NB);
+                const int valid = min(max(left - 2 * i, 0), 2);
+                const uint16_t* src = (of_v ? p.v_norms : p.k_norms) + (valid ? (row0 + t0) * NB + 2 * i : row0 * NB);
+                cp_async4(ring + (uint32_t)islot * kSlot + 32u * kStride + (uint32_t)(of_v * 64 * NB + 4 * i), src,
+                          2u * (uint32_t)valid);
+              }
+            }
           }
           cp_commit();
           if (++islot == depth) islot = 0;
@@ -1016,10 +1045,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           __syncwarp();
           uint32_t w[4 * B];
           read_codes<B>(ring + (uint32_t)cslot * kSlot + (uint32_t)(lane * kStride), w);
+          uint32_t nk[NB], nv[NB];  // this position's norms, fp16 bits
+          if (!side && item % NB == 0) {
+            const uint16_t* nrm = reinterpret_cast<const uint16_t*>(gen(ring + (uint32_t)cslot * kSlot + 32u * kStride)) + lane * NB;
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk) {
+              nk[blk] = nrm[blk];
+              nv[blk] = nrm[32 * NB + blk];
+            }
+          }
           if (++cslot == depth) cslot = 0;
           wait(emptyb + stage, ephase);
+          // The softmax warps read the norms of tile n - 4 before they free its
+          // S stage, which the product of tile n - 2 waited for, as this stage
+          // did for that product.
+          if (!side && item % NB == 0) {
+            float* dst = miscf + M::kNorm + (tile_no & 3) * NB * 2 * kTok + tok;
+#pragma unroll
+            for (int blk = 0; blk < NB; ++blk) {
+              dst[blk * 2 * kTok] = __half2float(__ushort_as_half((unsigned short)nk[blk]));
+              dst[blk * 2 * kTok + kTok] = __half2float(__ushort_as_half((unsigned short)nv[blk]));
+            }
+            ++tile_no;
+          }
           if (side) {
-            expand_to_smem<B>(w, pl.vt + stage * 2 * kPanel + (uint32_t)tok * 128u, tok, lane_base);
+            expand_to_smem<B>(w, pl.vt + stage * 2 * kPanel + (uint32_t)tok * 128u + (uint32_t)((tok & 7) << 4), lane_base);
             fence_async_smem();
           } else {
             tc_after();
@@ -1048,8 +1098,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     // loop bounds are warp-uniform, so that they stay in uniform registers: an
     // MMA of these shapes takes 32 to 64 cycles, and moving its descriptors
     // into place must not take longer.
-    regs_dec<kRegsMma>();
-    if (warp == 16) {
+    regs_dec<Ro::kMma>();
+    if (warp == Ro::kMmaWarp) {
       constexpr uint32_t id_s = mma_desc(N, false, false);
       uint32_t ks = 0, kph = 0, tile_no = 0, seg_no = 0;
       const uint64_t dq = smem_desc(pl.q, 16, 1024);
@@ -1086,7 +1136,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         x = sg.begin + sg.hi;
       }
-    } else if (warp == 17) {
+    } else if (warp == Ro::kMmaWarp + 1) {
       constexpr uint32_t id_o = mma_desc(N, true, true);
       uint32_t vs = 0, vph = 0, tile_no = 0;
       const uint64_t dv = smem_desc(pl.vt, kPanel, 1024), dp = smem_desc(pl.pt, kPanel, 1024);
@@ -1128,7 +1178,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 16)
+  if (warp == Ro::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
   // ---- rows of empty sequences are zero
   if (misc[M::kAnyEmpty]) {
@@ -1281,9 +1331,9 @@ bool plan(const TreeParams& p, Plan& pl) {
     pl.vt = take(2 * kPanel * t[0], 1024);
     pl.q = take((uint32_t)(4 * NB * N * 128), 1024);
     pl.pt = take((uint32_t)(t[1] * NB * ((N + 63) / 64)) * kPanel, 1024);
-    for (int w = 0; w < 8; ++w) pl.ring[w] = take(slot_bytes(w < 4 ? p.k_bits : p.v_bits) * t[2], 128);
+    for (int w = 0; w < 8; ++w) pl.ring[w] = take(slot_bytes(w < 4 ? p.k_bits : p.v_bits, w < 4 ? NB : 0) * t[2], 128);
     pl.bar = take(8 * kBars, 128);
-    pl.misc = take(4 * Misc<N>::kWords, 128);
+    pl.misc = take(4 * Misc<NB, N>::kWords, 128);
     pl.prefix = take(4u * (uint32_t)(p.batch + 1), 128);
     pl.bytes = end - kBase;
     if (ok) return true;
@@ -1320,8 +1370,8 @@ int run(Params& P, cudaStream_t stream) {
     return TQ_ERR_CUDA;
   cudaFuncAttributes attr_k;
   if (cudaFuncGetAttributes(&attr_k, kern) != cudaSuccess) return TQ_ERR_CUDA;
-  if (attr_k.numRegs < kRegsLaunch) return TQ_ERR_UNSUPPORTED;  // the register split would never be granted
-  kern<<<grid, kThreads, P.pl.bytes, stream>>>(P);
+  if (attr_k.numRegs < Roles<N>::kLaunch) return TQ_ERR_UNSUPPORTED;  // the register split would never be granted
+  kern<<<grid, Roles<N>::kThreads, P.pl.bytes, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
   if (grid == 1) return TQ_OK;  // no cut
   cudaLaunchConfig_t cfg = {};
