@@ -160,7 +160,7 @@ size_t tq_tree_workspace_size(const tq_kv_desc* desc, int q_heads, int n_q) {
   if (desc->head_dim > tq::kMaxDecodeHeadDim || desc->batch > tq::kMaxBatch) return 0;
   if (q_heads < desc->kv_heads || q_heads % desc->kv_heads != 0) return 0;
   if (n_q < 1 || n_q > TQ_MAX_TREE_NODES) return 0;
-  return tq::tree_workspace_bytes(desc->batch, desc->head_dim);
+  return tq::tree_workspace_bytes(desc->batch, desc->kv_heads, q_heads, desc->head_dim, n_q);
 }
 
 int tq_decode_attention_tree(const tq_kv_desc* desc, const tq_codebook* k_cb, const tq_codebook* v_cb,

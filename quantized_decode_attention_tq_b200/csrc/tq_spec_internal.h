@@ -78,7 +78,7 @@ struct TreeParams {
   float score_mult;  // scale * log2(e) / 128
   void* workspace;
 };
-size_t tree_workspace_bytes(int batch, int head_dim);
+size_t tree_workspace_bytes(int batch, int kv_heads, int q_heads, int head_dim, int n_q);
 int launch_tree(const TreeParams& p, cudaStream_t stream);
 
 // of tq_host.cpp

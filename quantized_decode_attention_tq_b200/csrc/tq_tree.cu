@@ -43,17 +43,17 @@ namespace {
 
 constexpr int kTok = 128;           // positions per tile
 // Roles by warpgroup (four warps): softmax groups of 128 threads, each with its
-// share of the row group's columns, then two that turn codes into fp16, then
-// one whose first two warps issue the MMAs.  Registers per thread at launch,
-// then by role: the shares must fit the launch's total.
+// share of the row group's columns; one group that turns K codes into fp16 and
+// one for V; one whose warps issue the score MMAs, the V MMAs and the copies.  Registers per thread
+// at launch, then by role: the shares must fit the launch's total.
 template <int N>
 struct Roles {
   static constexpr int kGroups = N >= 64 ? 4 : 2;
   static constexpr int kSoftWarps = 4 * kGroups, kCodeWarp = kSoftWarps, kMmaWarp = kSoftWarps + 8;
-  static constexpr int kWarps = kSoftWarps + 12, kThreads = 32 * kWarps;
+  static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
   static constexpr int kLaunch = kGroups == 4 ? 72 : 96;
-  static constexpr int kSoft = kGroups == 4 ? 80 : 136, kCodes = 72, kMma = kGroups == 4 ? 40 : 64;
-  static_assert(kGroups * kSoft + 2 * kCodes + kMma <= (kGroups + 3) * kLaunch, "register split");
+  static constexpr int kSoft = kGroups == 4 ? 80 : 136, kCodes = kGroups == 4 ? 64 : 72, kMma = kGroups == 4 ? 56 : 64;
+  static_assert(kGroups * kSoft + 2 * kCodes + kMma <= (kWarps / 4) * kLaunch, "register split");
 };
 constexpr int kMaxGrid = 256;       // CTAs at most (slots of the workspace)
 constexpr uint32_t kBase = 1024;    // shared-window address of dynamic shared memory
@@ -67,18 +67,33 @@ struct Plan {
   uint32_t bytes;
   uint32_t q, vt, pt;           // Q^ (hi, lo), V^ stages, P stages
   uint32_t lut_k, lut_v;
-  uint32_t ring[8];             // code rings of the eight dequantising warps
+  uint32_t ring_k, ring_v;      // code rings, a tile per slot
   uint32_t bar, misc, prefix;
   int v_stages, p_stages, depth;
+};
+
+// fp16 levels of a codebook by bytes: low bytes of levels 0-3 and 4-7, high bytes of the same
+struct Levels {
+  uint32_t lo0, lo1, hi0, hi1;
+};
+
+// What the join kernel needs of the unit that a CTA's range starts inside of:
+// parts first - 1 .. last (of the split) hold it.
+struct Join {
+  int b, kvh, hg, first, last;  // first = 0: the CTA's range starts with a unit, or the cut was not its first
 };
 
 struct Params {
   TreeParams t;
   Plan pl;
   float kscale, vscale;         // centroid scales
+  Levels klev;                  // K levels of 2- and 3-bit codes
   int n_hg;                     // row groups per kv-head
   FastDiv group;                // q_heads / kv_heads
-  int* ws_prefix;               // [batch + 1]
+  // workspace
+  float* ws_mul;                // [units] factor of a unit's scores
+  uint8_t* ws_q;                // [units] Q^ as it lies in shared memory
+  Join* ws_join;                // [grid]
   float* ws_ml;                 // [2 * grid][N][2]
   float* ws_acc;                // [2 * grid][N][D]
 };
@@ -125,47 +140,37 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait(int pending) {
-  if (pending >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
 __device__ __forceinline__ void bar_init(uint32_t a, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(count) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(uint32_t a) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
 }
+// Copy `bytes` (a multiple of 16) and let the barrier expect them.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t a, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.b32 %0, 1, 0, p; }"
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.b32 %0, 1, 0, p; }"
       : "=r"(ok)
-      : "r"(a), "r"(parity)
+      : "r"(a), "r"(parity), "n"(1000)
       : "memory");
   return ok != 0;
 }
-// Wait for a phase, for at most about a second: then the abort word is set,
-// every later wait returns at once, the loops run to their end on whatever the
-// buffers hold (all accesses stay in bounds), and the status word says so.
+// Wait for a phase, for at most about a second (2^20 tries of a microsecond):
+// then the abort word is set, every later wait returns at once, the loops run
+// to their end on whatever the buffers hold (all accesses stay in bounds), and
+// the status word says so.
 __device__ __forceinline__ void bar_wait(uint32_t a, uint32_t parity, uint32_t abort_word, uint32_t* status) {
-  if (bar_try(a, parity)) return;
-  const long long begin = clock64();
-  for (int i = 0; i < (1 << 26); ++i) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i) {
     if (bar_try(a, parity)) return;
     if (lds32(abort_word)) return;
-    if (clock64() - begin > 2000000000LL) break;
   }
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(abort_word), "r"(1) : "memory");
   if (status) atomicOr(status, TQ_DEV_INTERNAL);
@@ -233,6 +238,10 @@ __host__ __device__ constexpr uint32_t mma_desc(int n, bool a_mn, bool b_mn) {
 template <int R>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R, int Launch>
+__device__ __forceinline__ void regs_dec_to() {
+  if constexpr (R < Launch) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 template <int R>
 __device__ __forceinline__ void regs_dec() {
@@ -403,13 +412,30 @@ __device__ __forceinline__ uint32_t pair_addr(const uint32_t* w, int q, uint32_t
   return (x & (((1u << (2 * B)) - 1u) << 7)) | lane_base;
 }
 
+// Codes of 2 or 3 bits without a table in shared memory: eight codes are spread
+// to one per nibble (x + (x & high) * (2^s - 1) moves the high half up by s), a
+// byte permute picks the low bytes of four levels and another the high bytes,
+// and two more interleave them to fp16 pairs.
 template <int B>
-struct Slot {  // a ring slot: 32 positions, one block; padded so that 128-bit reads of 8 lanes hit distinct banks
-  static constexpr int kStride = B == 4 ? 80 : 48;
-};
-// K slots end with the positions' K norms and V norms, 64 bytes each per block.
-__host__ __device__ constexpr uint32_t slot_bytes(int bits, int norm_blocks) {
-  return 32u * (bits == 4 ? 80u : 48u) + 128u * (uint32_t)norm_blocks;
+__device__ __forceinline__ uint32_t spread8(const uint32_t* w, int g) {  // codes 8g .. 8g + 7 of the stream
+  if constexpr (B == 2) {
+    uint32_t x = (g & 1) ? w[g >> 1] >> 16 : w[g >> 1] & 0xFFFFu;
+    x += (x & 0xFF00u) * 255u;
+    x += (x & 0x00F000F0u) * 15u;
+    return x + (x & 0x0C0C0C0Cu) * 3u;
+  } else {
+    static_assert(B == 3, "spread codes");
+    const int pos = 24 * g, wi = pos >> 5, sh = pos & 31;
+    uint32_t x = sh == 8 ? w[wi] >> 8 : (sh == 0 ? w[wi] : __funnelshift_r(w[wi], w[wi + 1], sh)) & 0xFFFFFFu;
+    x += (x & 0xFFF000u) * 15u;
+    x += (x & 0x0FC00FC0u) * 3u;
+    return x + (x & 0x38383838u);
+  }
+}
+__device__ __forceinline__ void pick4(const Levels& t, uint32_t z, uint32_t& a, uint32_t& b) {
+  const uint32_t lo = __byte_perm(t.lo0, t.lo1, z), hi = __byte_perm(t.hi0, t.hi1, z);
+  a = __byte_perm(lo, hi, 0x5140);
+  b = __byte_perm(lo, hi, 0x7362);
 }
 
 // The codes of one position and block.
@@ -438,13 +464,22 @@ __device__ __forceinline__ void expand_to_smem(const uint32_t (&w)[4 * B], uint3
 }
 // Their values as 64 columns of this lane's row of tensor memory.
 template <int B>
-__device__ __forceinline__ void expand_to_tmem(const uint32_t (&w)[4 * B], uint32_t addr, uint32_t lane_base) {
+__device__ __forceinline__ void expand_to_tmem(const uint32_t (&w)[4 * B], uint32_t addr, uint32_t lane_base, const Levels& lv) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    float v[16];
+    uint32_t v[16];
+    if constexpr (B == 4) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(lds_table(pair_addr<B>(w, 16 * c + i, lane_base)));
-    tm_store<16>(addr + 16 * c, v);
+      for (int i = 0; i < 16; ++i) v[i] = lds_table(pair_addr<B>(w, 16 * c + i, lane_base));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t z = spread8<B>(w, 4 * c + i);
+        pick4(lv, z, v[4 * i], v[4 * i + 1]);
+        pick4(lv, z >> 16, v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+    tm_store<16>(addr + 16 * c, reinterpret_cast<const float(&)[16]>(v));
   }
   tc_wait_st();
 }
@@ -489,13 +524,13 @@ __device__ __forceinline__ long long out_row(const Params& P, int b, int kvh, in
 // --------------------------------------------------------------- the kernel --
 
 // barriers, two stages each but the last
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 14, kQFull = 16, kBars = 17 };
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 14, kQFull = 16,
+           kQFree = 17, kRingFull = 18, kRingFree = 24, kBars = 30 };  // rings: three slots for K, three for V
 
 // word offsets in the misc area
 template <int NB, int N>
 struct Misc {
-  static constexpr int kAbort = 0, kTmem = 1, kAnyEmpty = 2, kQmax = 4;      // [16]
-  static constexpr int kVmax = kQmax + 16;                                   // [16]
+  static constexpr int kAbort = 0, kTmem = 1, kAnyEmpty = 2, kVmax = 4;      // [16]
   static constexpr int kMoff = kVmax + 16;                                   // [N]
   static constexpr int kAlpha = kMoff + N;                                   // [N]
   static constexpr int kRed = kAlpha + N;                                    // [4][N]
@@ -553,7 +588,12 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       bar_init(bar(kPFull + s), kSoftWarps);
       bar_init(bar(kPFree + s), 1);
     }
-    bar_init(bar(kQFull), kSoftWarps);
+    bar_init(bar(kQFull), 1);
+    bar_init(bar(kQFree), 1);
+    for (int r = 0; r < 6; ++r) {
+      bar_init(bar(kRingFull + r), 1);
+      bar_init(bar(kRingFree + r), 4);
+    }
     misc[M::kAbort] = 0;
     misc[M::kAnyEmpty] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -578,7 +618,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       *reinterpret_cast<__half2*>(gen(base + 4u * (uint32_t)e)) = h;
     }
   };
-  fill(p.k_bits, p.kcent, P.kscale, pl.lut_k);
+  if (p.k_bits == 4 && pl.lut_k != pl.lut_v) fill(p.k_bits, p.kcent, P.kscale, pl.lut_k);
   fill(p.v_bits, p.vcent, P.vscale, pl.lut_v);
   bool empty = false;
   if (tid < 512) {
@@ -620,9 +660,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   }
   __syncthreads();
   const uint32_t tmem = misc[M::kTmem];
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= p.batch; i += kThreads) P.ws_prefix[i] = prefix[i];
-
   const int ub = p.kv_heads * P.n_hg;
   const Cut cut(prefix, p.batch, ub, gridDim.x);
   const long long begin = cut.start(blockIdx.x), end = blockIdx.x < cut.parts ? cut.start(blockIdx.x + 1) : begin;
@@ -635,6 +672,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   if (warp < kSoftWarps) {
     // ================================================================ softmax
     regs_inc<Ro::kSoft>();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the query kernel's factors
     const int quad = warp & 3, grp = warp >> 2, tk = 32 * quad + lane;
     const int c0 = grp * HC;  // first column of this group
     const uint32_t tm_lane = (uint32_t)(32 * quad) << 16;
@@ -649,102 +687,17 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       const Seg sg = find(cut, x, end, P.n_hg);
       const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
       const int nodes = clamp_nodes(p, sg.b), ctx = len - nodes;
-      // ---- the unit's rows: q^ = H (s o q), one power-of-two scale for all
-      // (|q^| <= 128 max |q|), split into two fp16 terms; column masks.  The
-      // loops stay rolled: this code runs once per unit, and fetching it cold
-      // would cost more than it saves (unrolled, 8 us for 64 rows).
-      named_sync(1, 32 * kSoftWarps);  // both groups are done with the unit before
-      float mul;
-      {
-        auto load_row = [&](int n, float (&v)[NB][4]) {
-          const int vl = sg.hg * N + n;
-          const long long row = vl < rows ? out_row(P, sg.b, sg.kvh, vl, nodes) : -1;
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
-            v[blk][0] = v[blk][1] = v[blk][2] = v[blk][3] = 0.0f;
-            if (row >= 0) {
-              const size_t e = (size_t)row * D + blk * kBlock + 4 * lane;
-              if (p.q_dtype == TQ_F32) {
-                const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
-                v[blk][0] = a.x; v[blk][1] = a.y; v[blk][2] = a.z; v[blk][3] = a.w;
-              } else {
-                const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + e);
-                float2 a, c;
-                if (p.q_dtype == TQ_F16) {
-                  a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
-                  c = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
-                } else {
-                  a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.x));
-                  c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.y));
-                }
-                v[blk][0] = a.x; v[blk][1] = a.y; v[blk][2] = c.x; v[blk][3] = c.y;
-              }
-            }
-          }
-        };
-        if (tid < N) {
-          const int vl = sg.hg * N + tid;
-          const int j = (int)P.group.div((uint32_t)vl);
-          uint64_t w = 0;
-          if (vl < rows && j < nodes)
-            w = __ldg(reinterpret_cast<const unsigned long long*>(p.tree) + (size_t)sg.b * p.n_q + j);
-          *reinterpret_cast<uint64_t*>(misc + M::kMask + 2 * tid) = w;
-        }
-        float mx = 0.0f;
-#pragma unroll 2
-        for (int n = warp; n < N; n += kSoftWarps) {
-          float v[NB][4];
-          load_row(n, v);
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = fabsf(v[blk][k]);
-              mx = fmaxf(mx, a < INFINITY ? a : 0.0f);  // elements that are not finite have no say
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0) miscf[M::kQmax + warp] = mx;
-        named_sync(1, 32 * kSoftWarps);
-#pragma unroll
-        for (int w = 0; w < kSoftWarps; ++w) mx = fmaxf(mx, miscf[M::kQmax + w]);
-        // 128 max |q| scaled to below 2^15
-        const int qe = mx > 0.0f ? max(ilogbf(mx) - 7, -110) : 0;
-        const float sc = ldexpf(1.0f, -qe);
-        mul = p.score_mult * ldexpf(1.0f, qe) / P.kscale;
-        const uint32_t sgn = p.sign_mask[lane >> 3] >> (4 * (lane & 7));
-#pragma unroll 2
-        for (int n = warp; n < N; n += kSoftWarps) {
-          float v[NB][4];
-          load_row(n, v);
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[blk][k] *= ((sgn >> k) & 1u) ? -sc : sc;
-          wht<NB>(v, lane);
-          // lane l holds dims 4l..4l+3: chunk l / 2 of the block, half l & 1
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
-            const uint32_t a = pl.q + (uint32_t)(2 * blk + (lane >> 4)) * kQPanel + (uint32_t)n * 128u +
-                               (uint32_t)((((lane >> 1) & 7) ^ (n & 7)) << 4) + 8u * (lane & 1);
-            const float(&y)[4] = v[blk];
-            __half2 h[2], r[2];
-            h[0] = __floats2half2_rn(y[0], y[1]);
-            h[1] = __floats2half2_rn(y[2], y[3]);
-            const float2 b0 = __half22float2(h[0]), b1 = __half22float2(h[1]);
-            r[0] = __floats2half2_rn(y[0] - b0.x, y[1] - b0.y);
-            r[1] = __floats2half2_rn(y[2] - b1.x, y[3] - b1.y);
-            sts64(a, *reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]));
-            sts64(a + 2 * NB * kQPanel, *reinterpret_cast<uint32_t*>(&r[0]), *reinterpret_cast<uint32_t*>(&r[1]));
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(kQFull));
+      named_sync(1, 32 * kSoftWarps);  // every group is done with the unit before
+      if (tid < N) {  // which nodes each row sees
+        const int vl = sg.hg * N + tid, j = (int)P.group.div((uint32_t)vl);
+        uint64_t w = 0;
+        if (vl < rows && j < nodes)
+          w = __ldg(reinterpret_cast<const unsigned long long*>(p.tree) + (size_t)sg.b * p.n_q + j);
+        *reinterpret_cast<uint64_t*>(misc + M::kMask + 2 * tid) = w;
       }
+      const float mul = *(volatile const float*)(P.ws_mul + (size_t)sg.b * ub + sg.r);
       if (tk < HC) miscf[M::kMoff + c0 + tk] = -kUnset;  // the references are kept negated
-      named_sync(gid, 128);
+      named_sync(1, 32 * kSoftWarps);
       float2 l[HC / 2];
 #pragma unroll
       for (int c = 0; c < HC / 2; ++c) l[c] = make_float2(0.0f, 0.0f);
@@ -993,105 +946,90 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
     }
   } else if (warp < Ro::kMmaWarp) {
     // ============================================================ dequantise
-    if constexpr (Ro::kCodes < Ro::kLaunch) regs_dec<Ro::kCodes>();
-    const int dq = warp - Ro::kCodeWarp, side = dq >> 2, quarter = dq & 3;
-    const uint32_t ring = pl.ring[dq];
-    auto work = [&](auto bits_tag) {
+    // A warp takes 32 positions of every tile from the code ring; the K warps'
+    // lanes also fetch their position's norms, a tile ahead.
+    regs_dec_to<Ro::kCodes, Ro::kLaunch>();
+    const int cw = warp - Ro::kCodeWarp, side = cw >> 2, quarter = cw & 3, tok = 32 * quarter + lane;
+    auto work = [&](auto bits_tag, auto side_tag) {
       constexpr int B = decltype(bits_tag)::value;
-      constexpr int kStride = Slot<B>::kStride;
-      const uint32_t kSlot = slot_bytes(B, side ? 0 : NB);
-      const uint8_t* codes = side ? p.v_codes : p.k_codes;
-      const uint32_t lane_base = (side ? pl.lut_v : pl.lut_k) + 4u * lane;
+      constexpr bool V = decltype(side_tag)::value;
+      constexpr uint32_t kRow = NB * 16 * B;  // bytes of a position
+      const uint32_t ring = (V ? pl.ring_v : pl.ring_k) + (uint32_t)tok * kRow, depth = (uint32_t)pl.depth;
+      const uint32_t lane_base = (V ? pl.lut_v : pl.lut_k) + 4u * lane;
       const uint32_t tm_k = tmem + ((uint32_t)(32 * quarter) << 16) + kColsK;
-      const int stages = side ? pl.v_stages : 2, depth = pl.depth;
-      const int full = side ? kVFull : kKFull, emptyb = side ? kVEmpty : kKEmpty;
-      const int tok = 32 * quarter + lane;
-      uint32_t tile_no = 0;
-      uint32_t stage = 0, ephase = 1;  // the first round finds the stages free
-      int cslot = 0, islot = 0;
+      const uint32_t v_row = pl.vt + (uint32_t)tok * 128u + (uint32_t)((tok & 7) << 4);
+      const uint32_t shift = V ? (uint32_t)pl.v_stages - 1 : 1u;
+      uint32_t slot = 0, slot_ph = 0, stage = 0, stage_ph = 1, tile_no = 0;
       for (long long x = begin; x < end;) {
         const Seg sg = find(cut, x, end, P.n_hg);
         const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
         const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
-        const int items = (sg.hi - sg.lo) * NB;
-        auto issue = [&](int item) {
-          if (item < items) {
-            const int t0 = (sg.lo + item / NB) * kTok + 32 * quarter, blk = item % NB;
+        const int tiles = sg.hi - sg.lo;
+        const int t_first = sg.lo * kTok + tok;  // this lane's position in the first tile
+        uint16_t kn[NB], vn[NB];
+        auto fetch_norms = [&](int i) {
+          const int t = t_first + i * kTok;
 #pragma unroll
-            for (int r = 0; r < B; ++r) {
-              const int c = lane + 32 * r, tt = c / B, part = c % B;
-              const bool ok = t0 + tt < len;
-              const uint8_t* src = codes + ((row0 + (ok ? t0 + tt : 0)) * NB + blk) * (16 * B) + 16 * part;
-              cp_async16(ring + (uint32_t)islot * kSlot + (uint32_t)(tt * kStride + 16 * part), src, ok ? 16u : 0u);
-            }
-            if (!side && blk == 0) {  // two norms per copy: 16 NB copies for K, then for V
-              const int left = (len - t0) * NB;  // norms from t0 to the end
-#pragma unroll
-              for (int r = 0; r < NB; ++r) {
-                const int c = lane + 32 * r, of_v = c / (16 * NB), i = c % (16 * NB);
-                const int valid = min(max(left - 2 * i, 0), 2);
-                const uint16_t* src = (of_v ? p.v_norms : p.k_norms) + (valid ? (row0 + t0) * NB + 2 * i : row0 * NB);
-                cp_async4(ring + (uint32_t)islot * kSlot + 32u * kStride + (uint32_t)(of_v * 64 * NB + 4 * i), src,
-                          2u * (uint32_t)valid);
-              }
+          for (int blk = 0; blk < NB; ++blk) {
+            kn[blk] = vn[blk] = 0;
+            if (t < len) {
+              kn[blk] = __ldg(p.k_norms + (row0 + t) * NB + blk);
+              vn[blk] = __ldg(p.v_norms + (row0 + t) * NB + blk);
             }
           }
-          cp_commit();
-          if (++islot == depth) islot = 0;
         };
-        for (int i = 0; i < depth; ++i) issue(i);
-        for (int item = 0; item < items; ++item) {
-          cp_wait(depth - 1);
-          __syncwarp();
-          uint32_t w[4 * B];
-          read_codes<B>(ring + (uint32_t)cslot * kSlot + (uint32_t)(lane * kStride), w);
-          uint32_t nk[NB], nv[NB];  // this position's norms, fp16 bits
-          if (!side && item % NB == 0) {
-            const uint16_t* nrm = reinterpret_cast<const uint16_t*>(gen(ring + (uint32_t)cslot * kSlot + 32u * kStride)) + lane * NB;
+        if (!V) fetch_norms(0);
+        for (int i = 0; i < tiles; ++i, ++tile_no) {
+          wait(kRingFull + (V ? 3 : 0) + (int)slot, slot_ph);
 #pragma unroll
-            for (int blk = 0; blk < NB; ++blk) {
-              nk[blk] = nrm[blk];
-              nv[blk] = nrm[32 * NB + blk];
+          for (int blk = 0; blk < NB; ++blk) {
+            uint32_t w[4 * B];
+            read_codes<B>(ring + slot * (kTok * kRow) + (uint32_t)(blk * 16 * B), w);
+            if (blk == NB - 1) {  // this warp has read the slot
+              __syncwarp();
+              if (lane == 0) bar_arrive(bar(kRingFree + (V ? 3 : 0) + (int)slot));
             }
-          }
-          if (++cslot == depth) cslot = 0;
-          wait(emptyb + stage, ephase);
-          // The softmax warps read the norms of tile n - 4 before they free its
-          // S stage, which the product of tile n - 2 waited for, as this stage
-          // did for that product.
-          if (!side && item % NB == 0) {
-            float* dst = miscf + M::kNorm + (tile_no & 3) * NB * 2 * kTok + tok;
+            wait((V ? kVEmpty : kKEmpty) + stage, stage_ph);
+            if constexpr (V) {
+              expand_to_smem<B>(w, v_row + stage * 2 * kPanel, lane_base);
+              fence_async_smem();
+            } else {
+              tc_after();
+              if (blk == 0) {
+                // The softmax warps read the norms of tile n - 4 before they
+                // free its S stage, which the product of tile n - 2 waited
+                // for, as this stage did for that product.
+                float* dst = miscf + M::kNorm + (tile_no & 3u) * NB * 2 * kTok + tok;
 #pragma unroll
-            for (int blk = 0; blk < NB; ++blk) {
-              dst[blk * 2 * kTok] = __half2float(__ushort_as_half((unsigned short)nk[blk]));
-              dst[blk * 2 * kTok + kTok] = __half2float(__ushort_as_half((unsigned short)nv[blk]));
+                for (int k = 0; k < NB; ++k) {
+                  dst[k * 2 * kTok] = __half2float(__ushort_as_half(kn[k]));
+                  dst[k * 2 * kTok + kTok] = __half2float(__ushort_as_half(vn[k]));
+                }
+                if (i + 1 < tiles) fetch_norms(i + 1);
+              }
+              expand_to_tmem<B>(w, tm_k + stage * 64, lane_base, P.klev);
+              tc_before();
             }
-            ++tile_no;
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar((V ? kVFull : kKFull) + stage));
+            stage = (stage + 1) & shift;
+            stage_ph ^= stage == 0 ? 1u : 0u;
           }
-          if (side) {
-            expand_to_smem<B>(w, pl.vt + stage * 2 * kPanel + (uint32_t)tok * 128u + (uint32_t)((tok & 7) << 4), lane_base);
-            fence_async_smem();
-          } else {
-            tc_after();
-            expand_to_tmem<B>(w, tm_k + stage * 64, lane_base);
-            tc_before();
-          }
-          __syncwarp();
-          if (lane == 0) bar_arrive(bar(full + stage));
-          issue(item + depth);
-          if (++stage == (uint32_t)stages) {
-            stage = 0;
-            ephase ^= 1;
+          if (++slot == depth) {
+            slot = 0;
+            slot_ph ^= 1;
           }
         }
         x = sg.begin + sg.hi;
       }
-      cp_wait(0);
     };
-    const int bits = side ? p.v_bits : p.k_bits;
-    if (bits == 2) work(std::integral_constant<int, 2>{});
-    else if (bits == 3) work(std::integral_constant<int, 3>{});
-    else work(std::integral_constant<int, 4>{});
+    auto by_bits = [&](int bits, auto side_tag) {
+      if (bits == 2) work(std::integral_constant<int, 2>{}, side_tag);
+      else if (bits == 3) work(std::integral_constant<int, 3>{}, side_tag);
+      else work(std::integral_constant<int, 4>{}, side_tag);
+    };
+    if (side) by_bits(p.v_bits, std::true_type{});
+    else by_bits(p.k_bits, std::false_type{});
   } else {
     // ================================================================= MMAs
     // Warp 16 issues the score products, warp 17 the V sums.  Descriptors and
@@ -1134,6 +1072,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
             kph ^= ks ^ 1;
           }
         }
+        if (elect_one()) tc_commit(bar(kQFree));
+        __syncwarp();
         x = sg.begin + sg.hi;
       }
     } else if (warp == Ro::kMmaWarp + 1) {
@@ -1172,6 +1112,54 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       // nothing is in flight when tensor memory is freed (every S product was
       // waited for by the softmax warps)
       if (tile_no > 0) wait(kPFree + p_stage(tile_no - 1), p_phase(tile_no - 1));
+    } else if (warp == Ro::kMmaWarp + 2 && lane == 0) {
+      // Codes into the rings: a tile's positions are contiguous in the cache.
+      // Positions past the end keep what the slot held: any code is a level,
+      // and their weights are zero.
+      const uint32_t depth = (uint32_t)pl.depth;
+      uint32_t slot = 0, free_ph = 1;
+      for (long long x = begin; x < end;) {
+        const Seg sg = find(cut, x, end, P.n_hg);
+        const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
+        const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
+        for (int tile = sg.lo; tile < sg.hi; ++tile) {
+          const uint32_t rows = (uint32_t)min(len - tile * kTok, kTok);
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const uint32_t row_bytes = NB * 16u * (uint32_t)(side ? p.v_bits : p.k_bits);
+            const uint8_t* src = (side ? p.v_codes : p.k_codes) + (row0 + (size_t)tile * kTok) * row_bytes;
+            wait(kRingFree + 3 * side + (int)slot, free_ph);
+            fence_async_smem();  // the slot's reads before the copy
+            bulk_copy((side ? pl.ring_v : pl.ring_k) + slot * (kTok * row_bytes), src, rows * row_bytes,
+                      bar(kRingFull + 3 * side + (int)slot));
+          }
+          if (++slot == depth) {
+            slot = 0;
+            free_ph ^= 1;
+          }
+        }
+        x = sg.begin + sg.hi;
+      }
+      if (lds32(abort_word)) __nanosleep(1000000);  // copies may be in flight: they end by themselves
+    } else if (warp == Ro::kMmaWarp + 3 && lane == 0) {
+      // Q^ of each unit, as the query kernel left it; and the join's record
+      Join j{};
+      if (begin < end) {
+        const Seg sg = find(cut, begin, end, P.n_hg);
+        if (sg.lo > 0 && cut.part_of(sg.begin) == (long long)blockIdx.x - 1)
+          j = Join{sg.b, sg.kvh, sg.hg, (int)blockIdx.x, (int)cut.part_of(sg.begin + sg.nt - 1)};
+      }
+      P.ws_join[blockIdx.x] = j;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      asm volatile("fence.proxy.async;" ::: "memory");
+      uint32_t seg_no = 0;
+      for (long long x = begin; x < end; ++seg_no) {
+        const Seg sg = find(cut, x, end, P.n_hg);
+        wait(kQFree, (seg_no & 1) ^ 1);
+        bulk_copy(pl.q, P.ws_q + ((size_t)sg.b * ub + sg.r) * (4 * NB * kQPanel), 4 * NB * kQPanel, bar(kQFull));
+        x = sg.begin + sg.hi;
+      }
+      if (lds32(abort_word)) __nanosleep(1000000);
     }
   }
 
@@ -1192,28 +1180,113 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   }
 }
 
-// Join of the units that a cut went through.  Block (c, g): boundary c of the
-// split, rows 8 g .. 8 g + 7; only a unit's first inner boundary does it.
+// The rows of every unit, ready for the score products: q^ = H (s o q) under
+// one power-of-two scale (|q^| <= 128 max |q|, scaled to below 2^15), split into
+// two fp16 terms, in the layout of the kernel's Q^ buffer.  One CTA per unit.
 template <int NB, int N>
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Params P, int grid) {
+__global__ void __launch_bounds__(512) query_kernel(const __grid_constant__ Params P) {
+  constexpr int D = NB * kBlock, kWarpsQ = 16;
+  constexpr uint32_t kQPanel = N * 128;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float wmax[kWarpsQ];
+  const TreeParams& p = P.t;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ub = p.kv_heads * P.n_hg, b = (int)(blockIdx.x / (unsigned)ub), r = (int)(blockIdx.x % (unsigned)ub);
+  const int kvh = r / P.n_hg, hg = r % P.n_hg, nodes = clamp_nodes(p, b), rows = (int)P.group.d * p.n_q;
+  constexpr int RW = (N + kWarpsQ - 1) / kWarpsQ;  // rows of a warp
+  float v[RW][NB][4];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const int n = warp + kWarpsQ * i, vl = hg * N + n;
+    const long long row = n < N && vl < rows ? out_row(P, b, kvh, vl, nodes) : -1;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      v[i][blk][0] = v[i][blk][1] = v[i][blk][2] = v[i][blk][3] = 0.0f;
+      if (row < 0) continue;
+      const size_t e = (size_t)row * D + blk * kBlock + 4 * lane;
+      if (p.q_dtype == TQ_F32) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
+        v[i][blk][0] = a.x; v[i][blk][1] = a.y; v[i][blk][2] = a.z; v[i][blk][3] = a.w;
+      } else {
+        const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + e);
+        float2 a, c;
+        if (p.q_dtype == TQ_F16) {
+          a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+          c = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+        } else {
+          a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.x));
+          c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h.y));
+        }
+        v[i][blk][0] = a.x; v[i][blk][1] = a.y; v[i][blk][2] = c.x; v[i][blk][3] = c.y;
+      }
+    }
+  }
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = fabsf(v[i][blk][k]);
+        mx = fmaxf(mx, a < INFINITY ? a : 0.0f);  // elements that are not finite have no say
+      }
+  mx = warp_max(mx);
+  if (lane == 0) wmax[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarpsQ; ++w) mx = fmaxf(mx, wmax[w]);
+  const int qe = mx > 0.0f ? max(ilogbf(mx) - 7, -110) : 0;
+  const float sc = ldexpf(1.0f, -qe);
+  if (threadIdx.x == 0) P.ws_mul[blockIdx.x] = p.score_mult * ldexpf(1.0f, qe) / P.kscale;
+  const uint32_t sgn = p.sign_mask[lane >> 3] >> (4 * (lane & 7));
+  uint8_t* image = P.ws_q + (size_t)blockIdx.x * (4 * NB * kQPanel);
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const int n = warp + kWarpsQ * i;
+    if (n >= N) break;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i][blk][k] *= ((sgn >> k) & 1u) ? -sc : sc;
+    wht<NB>(v[i], lane);
+    // lane l holds dims 4l..4l+3: chunk l / 2 of the block, half l & 1
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      uint8_t* a = image + (uint32_t)(2 * blk + (lane >> 4)) * kQPanel + (uint32_t)n * 128u +
+                   (uint32_t)((((lane >> 1) & 7) ^ (n & 7)) << 4) + 8u * (lane & 1);
+      const float(&y)[4] = v[i][blk];
+      __half2 h[2], t[2];
+      h[0] = __floats2half2_rn(y[0], y[1]);
+      h[1] = __floats2half2_rn(y[2], y[3]);
+      const float2 b0 = __half22float2(h[0]), b1 = __half22float2(h[1]);
+      t[0] = __floats2half2_rn(y[0] - b0.x, y[1] - b0.y);
+      t[1] = __floats2half2_rn(y[2] - b1.x, y[3] - b1.y);
+      *reinterpret_cast<uint2*>(a) = make_uint2(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]));
+      *reinterpret_cast<uint2*>(a + 2 * NB * kQPanel) =
+          make_uint2(*reinterpret_cast<uint32_t*>(&t[0]), *reinterpret_cast<uint32_t*>(&t[1]));
+    }
+  }
+}
+
+// Join of the units that a cut went through.  Block (c, g): the unit that CTA
+// c + 1 starts inside of (its first cut), rows 8 g .. 8 g + 7.
+template <int NB, int N>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params P) {
   constexpr int D = NB * kBlock;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeParams& p = P.t;
   const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const Cut cut(P.ws_prefix, p.batch, p.kv_heads * P.n_hg, grid);
-  const long long c = blockIdx.x + 1;
-  if (c >= cut.parts) return;
-  const long long x = cut.start(c);
-  const Seg sg = find(cut, x, cut.total, P.n_hg);
-  if (sg.lo == 0 || cut.part_of(sg.begin) != c - 1) return;
-  const int vl = sg.hg * N + n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Join jn = P.ws_join[blockIdx.x + 1];
+  if (jn.first == 0) return;
+  const int vl = jn.hg * N + n;
   if (vl >= (int)P.group.d * p.n_q) return;
-  const long long row = out_row(P, sg.b, sg.kvh, vl, clamp_nodes(p, sg.b));
+  const long long row = out_row(P, jn.b, jn.kvh, vl, clamp_nodes(p, jn.b));
   if (row < 0) return;
   // part c - 1 holds the unit's first tiles (its last segment: slot 2 (c-1) + 1),
   // parts c, c + 1, ... the rest (their first segments: slots 2 c', ...)
-  const long long last = cut.part_of(sg.begin + sg.nt - 1);
-  const int parts = (int)(last - c) + 2;
+  const long long c = jn.first;
+  const int parts = jn.last - jn.first + 2;
   auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
   float top = -INFINITY, l = 0.0f;
   float v[NB][4] = {};
@@ -1285,6 +1358,16 @@ float centroid_scale(const float* cent, int bits) {
   return best;
 }
 
+Levels level_bytes(const float* cent, float scale, int bits) {
+  uint32_t w[4] = {0, 0, 0, 0};
+  for (int j = 0; j < (1 << bits) && j < 8; ++j) {
+    const uint16_t h = __half_as_ushort(__float2half_rn(cent[j] * scale));
+    w[j >> 2] |= (uint32_t)(h & 255u) << (8 * (j & 3));
+    w[2 + (j >> 2)] |= (uint32_t)(h >> 8) << (8 * (j & 3));
+  }
+  return Levels{w[0], w[1], w[2], w[3]};
+}
+
 // First-fit placement in the shared window.
 struct Place {
   uint32_t lo[16], hi[16];
@@ -1311,7 +1394,7 @@ struct Place {
 template <int NB, int N>
 bool plan(const TreeParams& p, Plan& pl) {
   // in order of preference: stages of V^ and P, slots of a code ring
-  static const int tries[5][3] = {{2, 2, 3}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}};
+  static const int tries[6][3] = {{2, 2, 3}, {2, 2, 2}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}};
   for (const auto& t : tries) {
     pl = Plan{};
     Place at;
@@ -1326,12 +1409,17 @@ bool plan(const TreeParams& p, Plan& pl) {
     pl.v_stages = t[0];
     pl.p_stages = t[1];
     pl.depth = t[2];
-    pl.lut_k = take(128u << (2 * p.k_bits), 128u << (2 * p.k_bits));
+    // tables: V's, and K's for 4-bit codes, one for both where the levels are
     pl.lut_v = take(128u << (2 * p.v_bits), 128u << (2 * p.v_bits));
+    if (p.k_bits == 4) {
+      const bool same = p.v_bits == 4 && memcmp(p.kcent, p.vcent, sizeof(p.kcent)) == 0;
+      pl.lut_k = same ? pl.lut_v : take(128u << (2 * p.k_bits), 128u << (2 * p.k_bits));
+    }
     pl.vt = take(2 * kPanel * t[0], 1024);
     pl.q = take((uint32_t)(4 * NB * N * 128), 1024);
     pl.pt = take((uint32_t)(t[1] * NB * ((N + 63) / 64)) * kPanel, 1024);
-    for (int w = 0; w < 8; ++w) pl.ring[w] = take(slot_bytes(w < 4 ? p.k_bits : p.v_bits, w < 4 ? NB : 0) * t[2], 128);
+    pl.ring_k = take(kTok * NB * 16u * (uint32_t)(p.k_bits * t[2]), 128);
+    pl.ring_v = take(kTok * NB * 16u * (uint32_t)(p.v_bits * t[2]), 128);
     pl.bar = take(8 * kBars, 128);
     pl.misc = take(4 * Misc<NB, N>::kWords, 128);
     pl.prefix = take(4u * (uint32_t)(p.batch + 1), 128);
@@ -1360,30 +1448,42 @@ int run(Params& P, cudaStream_t stream) {
   if (sm_count(&sms) != TQ_OK) return TQ_ERR_CUDA;
   const int grid = (int)min(min((long long)sms, (long long)kMaxGrid), tiles);
   char* ws = static_cast<char*>(p.workspace);
-  P.ws_prefix = reinterpret_cast<int*>(ws);
-  ws += ((size_t)(p.batch + 1) * 4 + 255) / 256 * 256;
+  const size_t units = (size_t)p.batch * p.kv_heads * P.n_hg;
+  P.ws_mul = reinterpret_cast<float*>(ws);
+  ws += (units * 4 + 255) / 256 * 256;
+  P.ws_join = reinterpret_cast<Join*>(ws);
+  ws += kMaxGrid * 32;
   P.ws_ml = reinterpret_cast<float*>(ws);
   ws += (size_t)2 * kMaxGrid * N * 2 * 4;
   P.ws_acc = reinterpret_cast<float*>(ws);
+  ws += (size_t)2 * kMaxGrid * N * NB * kBlock * 4;
+  P.ws_q = reinterpret_cast<uint8_t*>(ws);
   auto kern = tree_kernel<NB, N>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn) != cudaSuccess)
     return TQ_ERR_CUDA;
   cudaFuncAttributes attr_k;
   if (cudaFuncGetAttributes(&attr_k, kern) != cudaSuccess) return TQ_ERR_CUDA;
   if (attr_k.numRegs < Roles<N>::kLaunch) return TQ_ERR_UNSUPPORTED;  // the register split would never be granted
-  kern<<<grid, Roles<N>::kThreads, P.pl.bytes, stream>>>(P);
+  // The kernel's set-up runs beside the query kernel, the join kernel's launch
+  // beside the kernel's end (programmatic dependent launches).
+  query_kernel<NB, N><<<(unsigned)units, 512, 0, stream>>>(P);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
-  if (grid == 1) return TQ_OK;  // no cut
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid - 1), N / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, merge_kernel<NB, N>, P, grid) != cudaSuccess) return TQ_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(Roles<N>::kThreads);
+  cfg.dynamicSmemBytes = P.pl.bytes;
+  if (cudaLaunchKernelEx(&cfg, kern, P) != cudaSuccess) return TQ_ERR_CUDA;
+  if (grid == 1) return TQ_OK;  // no cut
+  cfg.gridDim = dim3((unsigned)(grid - 1), N / 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<NB, N>, P) != cudaSuccess) return TQ_ERR_CUDA;
   return TQ_OK;
 }
 
@@ -1397,17 +1497,22 @@ int pick(Params& P, cudaStream_t stream) {
       if (st != TQ_ERR_UNSUPPORTED) return st;
     }
   }
-  if (!plan<NB, N>(P.t, P.pl)) return TQ_ERR_UNSUPPORTED;
-  return run<NB, N>(P, stream);
+  if (plan<NB, N>(P.t, P.pl)) return run<NB, N>(P, stream);
+  return TQ_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 }  // namespace tree
 
-size_t tree_workspace_bytes(int batch, int head_dim) {
-  // the widest row group's slots: N * head_dim is 128 * 128 at most
-  const size_t n = head_dim == kBlock ? 128 : 64;
-  return ((size_t)(batch + 1) * 4 + 255) / 256 * 256 + (size_t)2 * tree::kMaxGrid * n * (head_dim + 2) * 4;
+size_t tree_workspace_bytes(int batch, int kv_heads, int q_heads, int head_dim, int n_q) {
+  // slots of the widest row group, and Q^ of every unit (two fp16 terms); the
+  // rows of a kv-head fill whole row groups
+  const size_t rows = (size_t)(q_heads / kv_heads) * n_q, wide = head_dim == kBlock ? 128 : 64;
+  size_t n = 16;
+  while (n < rows && n < wide) n *= 2;
+  const size_t padded = (rows + n - 1) / n * n, units16 = (size_t)batch * kv_heads * ((rows + 15) / 16);
+  return (units16 * 4 + 255) / 256 * 256 + tree::kMaxGrid * 32 + (size_t)2 * tree::kMaxGrid * n * (head_dim + 2) * 4 +
+         (size_t)batch * kv_heads * padded * head_dim * 4;
 }
 
 int launch_tree(const TreeParams& t, cudaStream_t stream) {
@@ -1415,6 +1520,7 @@ int launch_tree(const TreeParams& t, cudaStream_t stream) {
   P.t = t;
   P.kscale = tree::centroid_scale(t.kcent, t.k_bits);
   P.vscale = tree::centroid_scale(t.vcent, t.v_bits);
+  P.klev = tree::level_bytes(t.kcent, P.kscale, t.k_bits);
   return t.head_dim == kBlock ? tree::pick<1, 16>(P, stream) : tree::pick<2, 16>(P, stream);
 }
 
