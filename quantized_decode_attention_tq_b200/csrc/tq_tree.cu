@@ -1332,30 +1332,54 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
 // --------------------------------------------------------------- host side --
 
 // A factor for a codebook's levels that makes their rounding to fp16 small:
-// the best of 256 in [1, 2), by the sum of squared errors.  The kernel divides
-// it out in fp32.
-float centroid_scale(const float* cent, int bits) {
-  const int half = 1 << (bits - 1);
-  float best = 1.0f, least = INFINITY;
-  for (int k = 0; k < 256; ++k) {
-    const float a = 1.0f + k * (1.0f / 256.0f);
+// the best of 8192 in [1, 2), by the mean squared error over N(0,1) (levels of
+// 2, 3, 4 bits: 0.7e-5, 1.6e-5, 4.9e-5 of their size, against 2e-4 unscaled).
+// The kernel divides it out in fp32.
+float find_scale(const float* cent, int levels) {
+  float weight[16], best = 1.0f, least = INFINITY;
+  for (int j = 0; j < levels; ++j) {  // density at the level times the width of its cell
+    const float lo = j > 0 ? cent[j - 1] : 2.0f * cent[j] - cent[j + 1];
+    const float hi = j + 1 < levels ? cent[j + 1] : 2.0f * cent[j] - cent[j - 1];
+    weight[j] = std::exp(-0.5f * cent[j] * cent[j]) * std::fabs(hi - lo) + 1e-6f;
+  }
+  for (int k = 0; k < 8192; ++k) {
+    const float a = 1.0f + k * (1.0f / 8192.0f), stop = least * a * a;
     float err = 0.0f;
-    for (int j = 0; j < half; ++j) {
-      const float x = cent[half + j] * a;
+    for (int j = levels - 1; j >= 0 && err < stop; --j) {
+      const float x = cent[j] * a;
       uint32_t u;
       memcpy(&u, &x, 4);
       u = (u + 0xFFFu + ((u >> 13) & 1u)) & ~0x1FFFu;  // 10 mantissa bits, to nearest even
       float r;
       memcpy(&r, &u, 4);
-      err += (r - x) * (r - x);
+      err += weight[j] * (r - x) * (r - x);
     }
-    err /= a * a;
-    if (err < least) {
-      least = err;
+    if (err < stop) {
+      least = err / (a * a);
       best = a;
     }
   }
   return best;
+}
+
+// The search takes some 0.1 ms, so a thread keeps the last factors it found,
+// by the levels' values.
+float centroid_scale(const float* cent, int bits) {
+  struct Known {
+    float cent[16], scale;
+    int bits;
+  };
+  static thread_local Known known[4] = {};
+  static thread_local int next = 0;
+  const size_t size = sizeof(float) << bits;
+  for (const Known& k : known)
+    if (k.bits == bits && memcmp(k.cent, cent, size) == 0) return k.scale;
+  Known& k = known[next];
+  next = (next + 1) & 3;
+  memcpy(k.cent, cent, size);
+  k.scale = find_scale(cent, 1 << bits);
+  k.bits = bits;
+  return k.scale;
 }
 
 Levels level_bytes(const float* cent, float scale, int bits) {
