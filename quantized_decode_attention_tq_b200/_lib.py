@@ -103,7 +103,7 @@ SIGNATURES = {
 c_double = ctypes.c_double
 SPEC_SIGNATURES = {
     "tq_make_rope": (c_int, [c_int, c_int, c_double, c_int, c_double, c_double, c_double, c_double, _P(Rope)]),
-    "tq_qk_norm_rope": (c_int, [_P(Rope), c_int, c_int, c_int, _P(Rows), _P(Rows), _P(Rows), c_int, c_int, c_int,
+    "tq_qk_norm_rope": (c_int, [_P(Rope), c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
                                 c_int, c_float, c_float, c_void_p, c_void_p, c_void_p]),
     "tq_tree_masks": (c_int, [c_void_p, c_int, c_void_p, c_void_p]),
     "tq_tree_workspace_size": (c_size_t, [_P(KVDesc), c_int, c_int]),

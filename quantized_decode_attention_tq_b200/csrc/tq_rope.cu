@@ -5,11 +5,12 @@
 //
 // Bound by HBM: every row is read once and written once and nothing else
 // moves.  A group of LPR lanes (8, 16 or 32 for rows of up to 128, 256, 512)
-// holds a row as two 8-element chunks per lane.  In the half layout (pairs
-// (i, i + rot/2)) with rot/2 a multiple of 8 the two chunks are the two halves
-// of the same pairs, and in the interleaved layout a chunk holds whole pairs,
-// so the rotation stays in the lane; other half-layout widths fetch each
-// element's partner from a shared copy of the row.
+// holds a row as two 8-element chunks per lane and loads the next row while it
+// works on one.  In the half layout (pairs (i, i + rot/2)) with rot/2 a
+// multiple of 8 the two chunks are the two halves of the same pairs, and in
+// the interleaved layout a chunk holds whole pairs, so the rotation stays in
+// the lane; other half-layout widths fetch each element's partner from a
+// shared copy of the row.
 //
 // The phase of (position, pair) is position * turns modulo 2^64, an exact
 // integer product; its top 32 bits, reduced to the nearest quarter turn, leave
@@ -25,6 +26,7 @@ namespace tq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kMaxTT = 8;
 
 template <int DT>
 struct Elem;
@@ -87,6 +89,23 @@ __device__ __forceinline__ float load_weight(const void* w, int dt, int i) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // cos and sin of 2 pi * phase / 2^64
 __device__ __forceinline__ float2 phase_cs(uint64_t phase) {
   const uint32_t top = (uint32_t)(phase >> 32);
@@ -98,210 +117,257 @@ __device__ __forceinline__ float2 phase_cs(uint64_t phase) {
   return (quarter & 2u) ? make_float2(-c1, -s1) : make_float2(c1, s1);
 }
 
-// Shared memory: cos and sin [TT][D / 2], weights [2][D], then (GEN) one row
-// of floats per group.
-template <int IN, int OUT, int LPR, bool GEN>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows,
-                                                            FastDiv by_seq) {
+// Where element e of a row or table lies in shared memory when lanes hold 16
+// consecutive ones: a word of padding per 16, so that lanes 16 elements apart
+// use different banks (and groups of lanes, 8 words apart, all 32).
+__device__ __forceinline__ int padded(int e) { return e + (e >> 4); }
+
+enum Layout { kHalves = 0, kNeighbours = 1, kAnyHalves = 2 };  // kAnyHalves: rot/2 not a multiple of 8
+
+// Shared memory: cos and sin [TT][pitch], weights [2][D], then (kAnyHalves) one
+// row of floats per group.
+template <int IN, int OUT, int LPR, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, IN == TQ_F32 || MODE == kAnyHalves ? 3 : 4)
+rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastDiv by_seq) {
+  constexpr bool GEN = MODE == kAnyHalves, INTER = MODE == kNeighbours, split = MODE == kHalves;
   constexpr int kGroups = kRopeThreads / LPR;
-  constexpr int VI = Elem<IN>::kVec, VO = Elem<OUT>::kVec;
+  constexpr int VI = Elem<IN>::kVec, VO = Elem<OUT>::kVec, kIn = IN == TQ_F32 ? 4 : 2, kOut = OUT == TQ_F32 ? 4 : 2;
+  struct Base {
+    const char* in;  // null: a token that is left alone
+    char* out;
+  };
+  struct Step {
+    long long in, out;  // bytes from one head to the next
+  };
+  __shared__ Base base[kMaxTT][4];
+  __shared__ Step step[4];
   extern __shared__ __align__(16) float sm[];
   const int D = p.head_dim, hp = p.rot_dim / 2, half_d = D / 2;
+  const int pitch = GEN ? half_d + half_d / 16 : half_d;  // of a token's table
   float* cos_t = sm;
-  float* sin_t = sm + TT * half_d;
-  float* wts = sm + 2 * TT * half_d;
+  float* sin_t = sm + TT * pitch;
+  float* wts = sm + 2 * TT * pitch;
   float* scratch = wts + 2 * D;
   const int tid = threadIdx.x, sub = tid % LPR, group = tid / LPR;
   const uint32_t n_tokens = (uint32_t)p.batch * (uint32_t)p.seq_new;
   const uint32_t tok0 = blockIdx.x * (uint32_t)TT;
   const int toks = (int)min((uint32_t)TT, n_tokens - tok0);
   const int items = toks * p.rows;
+  const float inv_d = 1.0f / (float)D;
+  const int end_q = p.side[0].heads, end_k = end_q + p.side[1].heads;
 
   // chunk indices of this lane (see the file comment)
   const int hc = hp / 8;
-  int ca, cb;
-  if (!GEN && !p.interleaved && sub < hc) {
-    ca = sub;
-    cb = sub + hc;
-  } else if (!GEN && !p.interleaved) {
-    ca = 2 * hc + 2 * (sub - hc);
-    cb = ca + 1;
-  } else {
-    ca = 2 * sub;
-    cb = ca + 1;
-  }
+  const int ca = split ? (sub < hc ? sub : 2 * hc + 2 * (sub - hc)) : 2 * sub;
+  const int cb = split && sub < hc ? sub + hc : ca + 1;
   const bool has = 16 * sub < D;  // rows of 384 leave the last lanes idle
+  const int m0 = 8 * sub;         // this lane's pairs m0 .. m0 + 7
+  const bool all = !GEN && m0 + 8 <= hp, some = !GEN && m0 < hp;  // all or some of them turn
 
-  struct Where {
-    const void* src;
-    int b, t, side, head;
-    bool live;
-  };
-  auto locate = [&](int item) {
-    Where w{};
-    const uint32_t tk = by_rows.div((uint32_t)item);
-    int r = item - (int)tk * p.rows;
-    const uint32_t token = tok0 + tk;
-    w.b = (int)by_seq.div(token);
-    w.t = (int)(token - (uint32_t)w.b * (uint32_t)p.seq_new);
-    w.side = 0;
-    if (r >= p.side[0].heads) {
-      r -= p.side[0].heads;
-      w.side = 1;
-      if (r >= p.side[1].heads) {
-        r -= p.side[1].heads;
-        w.side = 2;
+  // where each token's rows of each side begin
+  if (tid < 3 * toks) {
+    const int tk = tid / 3, s = tid - 3 * tk;
+    const RowSide& side = p.side[s];
+    const uint32_t token = tok0 + (uint32_t)tk;
+    const int b = (int)by_seq.div(token), t = (int)(token - (uint32_t)b * (uint32_t)p.seq_new);
+    Base x{nullptr, nullptr};
+    if (!p.n_tok || t < __ldg(p.n_tok + b)) {
+      const long long row = s == 0 ? ((long long)b * p.seq_new + t) * side.heads : (long long)b * side.heads * p.seq_new + t;
+      x.in = static_cast<const char*>(side.in) + (b * side.batch_stride + t * side.token_stride) * kIn;
+      x.out = static_cast<char*>(side.out) + row * (D * kOut);
+    }
+    base[tk][s] = x;
+    if (tk == 0) step[s] = Step{side.head_stride * kIn, (s == 0 ? 1LL : (long long)p.seq_new) * (D * kOut)};
+  }
+  __syncthreads();
+
+  struct Row {
+    uint4 a[VI], b[VI];
+    char* out;  // null: nothing to write
+    int token, side;
+  } cur;
+  auto load = [&](int item) {
+    const int tk = (int)by_rows.div((uint32_t)min(item, items - 1)), r = min(item, items - 1) - tk * p.rows;
+    const int s = r < end_q ? 0 : r < end_k ? 1 : 2, h = r - (s == 0 ? 0 : s == 1 ? end_q : end_k);
+    const Base x = base[tk][s];
+    const Step d = step[s];
+    cur.token = tk;
+    cur.side = s;
+    cur.out = item < items && has && x.in ? x.out + h * d.out : nullptr;
+    if (cur.out) {
+      const uint4* src = reinterpret_cast<const uint4*>(x.in + h * d.in);
+#pragma unroll
+      for (int i = 0; i < VI; ++i) {
+        cur.a[i] = __ldcs(src + ca * VI + i);
+        cur.b[i] = __ldcs(src + cb * VI + i);
       }
     }
-    w.head = r;
-    const RowSide& s = p.side[w.side];
-    const long long off = w.b * s.batch_stride + w.t * s.token_stride + r * s.head_stride;
-    w.src = static_cast<const char*>(s.in) + off * (IN == TQ_F32 ? 4 : 2);
-    w.live = !p.n_tok || w.t < __ldg(p.n_tok + w.b);
-    return w;
-  };
-  auto load = [&](const Where& w, uint4 (&a)[VI], uint4 (&b)[VI]) {
-    if (!has || !w.live) return;
-    const uint4* src = static_cast<const uint4*>(w.src);
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      a[i] = __ldcs(src + ca * VI + i);
-      b[i] = __ldcs(src + cb * VI + i);
-    }
   };
 
-  // the first rows' loads are in flight while the tables are filled
-  uint4 ra[VI] = {}, rb[VI] = {};
-  Where cur{};
-  if (group < items) {
-    cur = locate(group);
-    load(cur, ra, rb);
-  }
+  load(group);  // in flight while the tables are filled
   for (int i = tid; i < toks * hp; i += kRopeThreads) {
     const int tk = i / hp, m = i - tk * hp;
     const long long pos = __ldg(p.positions + tok0 + tk);
-    const float2 cs = phase_cs((uint64_t)pos * p.turns[m]);
-    cos_t[tk * half_d + m] = p.gain * cs.x;
-    sin_t[tk * half_d + m] = p.gain * cs.y;
+    const float2 c = phase_cs((uint64_t)pos * p.turns[m]);
+    const int at = tk * pitch + (GEN ? padded(m) : m);
+    cos_t[at] = p.gain * c.x;
+    sin_t[at] = p.gain * c.y;
   }
   if (p.norm)
     for (int i = tid; i < 2 * D; i += kRopeThreads) {
-      const void* w = p.side[i / D].weight;
-      wts[i] = (w ? load_weight(w, p.w_dtype, i % D) : 1.0f) + p.weight_bias;
+      const int s = i >= D ? 1 : 0;
+      const void* w = p.side[s].weight;
+      wts[i] = (w ? load_weight(w, p.w_dtype, i - s * D) : 1.0f) + p.weight_bias;
     }
   __syncthreads();
 
   for (int item = group; item - group < items; item += kGroups) {
-    const bool mine = item < items;
-    Where w = cur;
-    float xa[8], xb[8];
-    unpack8<IN>(ra, xa);
-    unpack8<IN>(rb, xb);
-    if (item + kGroups < items) {
-      cur = locate(item + kGroups);
-      load(cur, ra, rb);
-    }
-    const bool rotated = w.side < 2;
-    if (p.norm) {  // every lane takes part in the shuffles
-      float ss = 0.0f;
+    const int s = cur.side;
+    char* const out = cur.out;
+    const float* ct = cos_t + cur.token * pitch;
+    const float* st = sin_t + cur.token * pitch;
+    float u[8], v[8];  // halves: the two halves; neighbours: even and odd elements
+    {
+      float xa[8], xb[8];
+      unpack8<IN>(cur.a, xa);
+      unpack8<IN>(cur.b, xb);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(xa[k], xa[k], fmaf(xb[k], xb[k], ss));
-      if (!has || !mine) ss = 0.0f;
+      for (int k = 0; k < 8; ++k) {
+        u[k] = INTER ? (k < 4 ? xa[(2 * k) & 7] : xb[(2 * k) & 7]) : xa[k];
+        v[k] = INTER ? (k < 4 ? xa[(2 * k + 1) & 7] : xb[(2 * k + 1) & 7]) : xb[k];
+      }
+    }
+    load(item + kGroups);
+    if (p.norm) {  // every lane takes part in the shuffles
+      float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        q = fma2(make_float2(u[k], u[k + 1]), make_float2(u[k], u[k + 1]), q);
+        q = fma2(make_float2(v[k], v[k + 1]), make_float2(v[k], v[k + 1]), q);
+      }
+      float ss = out ? q.x + q.y : 0.0f;
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (rotated && has) {
-        const float inv = 1.0f / sqrtf(ss / (float)D + p.eps);
-        const float* wt = wts + w.side * D;
+      if (s < 2 && has) {
+        const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
+        const float2 i2 = make_float2(inv, inv);
+        const float4* wa = reinterpret_cast<const float4*>(wts + s * D + 8 * ca);
+        const float4* wb = reinterpret_cast<const float4*>(wts + s * D + 8 * cb);
+        const float4 a0 = wa[0], a1 = wa[1], b0 = wb[0], b1 = wb[1];
+        const float ea[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const float eb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          float wu[2], wv[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int e = k + j;
+            wu[j] = INTER ? (e < 4 ? ea[(2 * e) & 7] : eb[(2 * e) & 7]) : ea[e];
+            wv[j] = INTER ? (e < 4 ? ea[(2 * e + 1) & 7] : eb[(2 * e + 1) & 7]) : eb[e];
+          }
+          const float2 x = mul2(make_float2(u[k], u[k + 1]), mul2(make_float2(wu[0], wu[1]), i2));
+          const float2 y = mul2(make_float2(v[k], v[k + 1]), mul2(make_float2(wv[0], wv[1]), i2));
+          u[k] = x.x, u[k + 1] = x.y;
+          v[k] = y.x, v[k + 1] = y.y;
+        }
+      }
+    }
+    if (s < 2) {
+      if (all) {
+        const float4* c4 = reinterpret_cast<const float4*>(ct + m0);
+        const float4* n4 = reinterpret_cast<const float4*>(st + m0);
+        const float4 c0 = c4[0], c1 = c4[1], n0 = n4[0], n1 = n4[1];
+        const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+        const float2 sn[4] = {{n0.x, n0.y}, {n0.z, n0.w}, {n1.x, n1.y}, {n1.z, n1.w}};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 c = cs[k], n = sn[k];
+          const float2 x = make_float2(u[2 * k], u[2 * k + 1]), y = make_float2(v[2 * k], v[2 * k + 1]);
+          const float2 z = mul2(y, n), o = fma2(x, c, make_float2(-z.x, -z.y)), q = fma2(y, c, mul2(x, n));
+          u[2 * k] = o.x, u[2 * k + 1] = o.y;
+          v[2 * k] = q.x, v[2 * k + 1] = q.y;
+        }
+      } else if (some) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (m0 + k < hp) {
+            const float c = ct[m0 + k], n = st[m0 + k], x = u[k];
+            u[k] = x * c - v[k] * n;
+            v[k] = v[k] * c + x * n;
+          }
+      }
+    }
+    if constexpr (GEN) {  // u, v: the lane's 16 consecutive elements
+      float* copy = scratch + group * (D + D / 16);
+      if (has) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          xa[k] *= inv * wt[8 * ca + k];
-          xb[k] *= inv * wt[8 * cb + k];
+          copy[17 * sub + k] = u[k];
+          copy[17 * sub + 8 + k] = v[k];
         }
       }
-    }
-    const int tk = (int)by_rows.div((uint32_t)min(item, items - 1));
-    if (hp > 0) {
-      const float* ct = cos_t + tk * half_d;
-      const float* st = sin_t + tk * half_d;
-      if constexpr (GEN) {
-        float* row = scratch + group * (D + 4);
-        if (has) {
+      __syncwarp();
+      if (s < 2 && has) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            row[8 * ca + k] = xa[k];
-            row[8 * cb + k] = xb[k];
-          }
-        }
-        __syncwarp();
-        if (rotated && has) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int e = 16 * sub + k;
-            float& x = k < 8 ? xa[k & 7] : xb[k & 7];
-            if (e < hp) x = x * ct[e] - row[e + hp] * st[e];
-            else if (e < 2 * hp) x = x * ct[e - hp] + row[e - hp] * st[e - hp];
-          }
-        }
-        __syncwarp();
-      } else if (rotated && has) {
-        if (p.interleaved) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // pairs 8 sub + k: four in each chunk
-            const int m = 8 * sub + k;
-            float& a = k < 4 ? xa[(2 * k) & 7] : xb[(2 * k) & 7];
-            float& b = k < 4 ? xa[(2 * k + 1) & 7] : xb[(2 * k + 1) & 7];
-            if (m < hp) {
-              const float c = ct[m], s = st[m], a0 = a;
-              a = a0 * c - b * s;
-              b = b * c + a0 * s;
-            }
-          }
-        } else if (sub < hc) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float c = ct[8 * sub + k], s = st[8 * sub + k], a0 = xa[k];
-            xa[k] = a0 * c - xb[k] * s;
-            xb[k] = xb[k] * c + a0 * s;
+        for (int k = 0; k < 16; ++k) {
+          const int e = 16 * sub + k;
+          float& x = k < 8 ? u[k & 7] : v[k & 7];
+          if (e < 2 * hp) {
+            const int m = e < hp ? e : e - hp;
+            const float n = st[padded(m)];
+            x = fmaf(copy[padded(e < hp ? e + hp : m)], e < hp ? -n : n, x * ct[padded(m)]);
           }
         }
       }
+      __syncwarp();
     }
-    if (mine && has && w.live) {
-      const RowSide& s = p.side[w.side];
-      const size_t row = w.side == 0 ? ((size_t)w.b * p.seq_new + w.t) * s.heads + w.head
-                                     : ((size_t)w.b * s.heads + w.head) * p.seq_new + w.t;
-      uint4* dst = static_cast<uint4*>(s.out) + row * (size_t)(D / 8 * VO);
+    if (out) {
+      uint4* dst = reinterpret_cast<uint4*>(out);
       uint4 oa[VO], ob[VO];
-      pack8<OUT>(xa, oa);
-      pack8<OUT>(xb, ob);
+      float ya[8], yb[8];
 #pragma unroll
-      for (int i = 0; i < VO; ++i) {
-        dst[ca * VO + i] = oa[i];
-        dst[cb * VO + i] = ob[i];
+      for (int k = 0; k < 8; ++k) {
+        ya[k] = INTER ? (k & 1 ? v[k / 2] : u[k / 2]) : u[k];
+        yb[k] = INTER ? (k & 1 ? v[4 + k / 2] : u[4 + k / 2]) : v[k];
+      }
+      pack8<OUT>(ya, oa);
+      pack8<OUT>(yb, ob);
+#pragma unroll
+      for (int k = 0; k < VO; ++k) {
+        dst[ca * VO + k] = oa[k];
+        dst[cb * VO + k] = ob[k];
       }
     }
   }
 }
 
-template <int IN, int OUT, int LPR, bool GEN>
+template <int IN, int OUT, int LPR, int MODE>
 int run_rope(const RopeParams& p, cudaStream_t stream) {
-  // One token per CTA while the GPU is not full, then four: the table of
-  // cosines is filled by all threads at once.
+  // One token per CTA while that gives every SM no more than four CTAs, then
+  // more: the tables are filled by all threads at once.
+  constexpr int kGroups = kRopeThreads / LPR;
+  const int D = p.head_dim, pitch = MODE == kAnyHalves ? D / 2 + D / 32 : D / 2;
   const long long tokens = (long long)p.batch * p.seq_new;
-  const int TT = tokens > 4 * 148 * 4 ? 4 : 1;
-  const size_t smem = sizeof(float) * ((size_t)TT * p.head_dim + 2 * p.head_dim +
-                                       (GEN ? (size_t)(kRopeThreads / LPR) * (p.head_dim + 4) : 0));
-  rope_kernel<IN, OUT, LPR, GEN><<<(unsigned)((tokens + TT - 1) / TT), kRopeThreads, smem, stream>>>(
+  int TT = 1;
+  while (TT < kMaxTT && tokens > (long long)TT * 4 * 148) TT *= 2;
+  const size_t smem = sizeof(float) * ((size_t)2 * TT * pitch + 2 * D + (MODE == kAnyHalves ? kGroups * (D + D / 16) : 0));
+  rope_kernel<IN, OUT, LPR, MODE><<<(unsigned)((tokens + TT - 1) / TT), kRopeThreads, smem, stream>>>(
       p, TT, FastDiv::make((uint32_t)p.rows), FastDiv::make((uint32_t)p.seq_new));
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
+template <int IN, int OUT, int LPR>
+int dispatch_mode(const RopeParams& p, cudaStream_t stream) {
+  if (p.interleaved) return run_rope<IN, OUT, LPR, kNeighbours>(p, stream);
+  if ((p.rot_dim / 2) % 8 != 0) return run_rope<IN, OUT, LPR, kAnyHalves>(p, stream);
+  return run_rope<IN, OUT, LPR, kHalves>(p, stream);
+}
+
 template <int IN, int OUT>
 int dispatch_lpr(const RopeParams& p, cudaStream_t stream) {
-  const bool gen = p.rot_dim > 0 && !p.interleaved && (p.rot_dim / 2) % 8 != 0;
-  if (p.head_dim <= 128) return gen ? run_rope<IN, OUT, 8, true>(p, stream) : run_rope<IN, OUT, 8, false>(p, stream);
-  if (p.head_dim <= 256) return gen ? run_rope<IN, OUT, 16, true>(p, stream) : run_rope<IN, OUT, 16, false>(p, stream);
-  return gen ? run_rope<IN, OUT, 32, true>(p, stream) : run_rope<IN, OUT, 32, false>(p, stream);
+  if (p.head_dim <= 128) return dispatch_mode<IN, OUT, 8>(p, stream);
+  if (p.head_dim <= 256) return dispatch_mode<IN, OUT, 16>(p, stream);
+  return dispatch_mode<IN, OUT, 32>(p, stream);
 }
 
 template <int IN>

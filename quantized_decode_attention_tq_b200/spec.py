@@ -6,63 +6,81 @@ the calls run on the tensors' device and its current stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 
-from ._lib import (TQ_BF16, TQ_F16, TQ_F32, TQ_MAX_TREE_NODES, CacheBufs, Codebook, KVDesc, Rope, Rows, check, lib)
+from ._lib import TQ_BF16, TQ_F16, TQ_F32, TQ_MAX_TREE_NODES, CacheBufs, Codebook, KVDesc, Rope, check, lib
 from .api import Cache, VOutliers
 
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-_CODES = {}
+_ROWS = struct.Struct("PPPi4xqqq")  # tq_rows
+_torch = None
+_codes = {}
+
+
+def _setup():
+    global _torch
+    import torch
+    _codes.update({torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16})
+    _torch = torch
+    return torch
 
 
 def _code(dtype) -> int:
-    if not _CODES:
-        import torch
-        _CODES.update({torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16})
-    try:
-        return _CODES[dtype]
-    except KeyError:
-        raise ValueError(f"unsupported dtype {dtype}: fp32, fp16 or bf16") from None
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}: fp32, fp16 or bf16")
+    return code
 
 
-class _On:
-    """The device of a call's tensors: checks them, makes it current, gives the stream."""
+def _device(t, name) -> int:
+    """The device index that every tensor of the call must have."""
+    if _torch is None:
+        _setup()
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return d
 
-    def __init__(self, first, name):
-        if not first.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        self.device = first.device
 
-    def ptr(self, t, name, contiguous=True):
-        if t is None:
-            return None
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, like the other tensors of the call")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+def _ptr(t, name, dev, contiguous=True):
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, like the other tensors of the call")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def i32(self, t, name, shape):
-        if t is None:
-            return None
-        import torch
-        if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be int32 of shape {tuple(shape)}")
-        return self.ptr(t, name)
 
-    def call(self, fn, stream, *args):
-        import torch
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream must be on {self.device}, like the tensors of the call")
-        f = getattr(lib(), fn)
-        if torch.cuda.current_device() == self.device.index:
-            s = (stream or torch.cuda.current_stream()).cuda_stream
-            check(fn, f(*args, s))
-        else:
-            with torch.cuda.device(self.device):
-                s = (stream or torch.cuda.current_stream()).cuda_stream
-                check(fn, f(*args, s))
+def _i32(t, name, dev, shape):
+    if t is None:
+        return None
+    if t.dtype is not _torch.int32 or t.shape != shape:
+        raise ValueError(f"{name} must be int32 of shape {shape}")
+    return _ptr(t, name, dev)
+
+
+def _status(t, dev):
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.numel() < 1:
+        raise ValueError("status must be a one-element int32 tensor")
+    return _ptr(t, "status", dev)
+
+
+def _call(fn, dev, stream, *args):
+    """Run fn(*args, stream) with the tensors' device current."""
+    f, cuda = getattr(lib(), fn), _torch.cuda
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream must be on cuda:{dev}, like the tensors of the call")
+    if cuda.current_device() == dev:
+        st = f(*args, (cuda.current_stream() if stream is None else stream).cuda_stream)
+    else:
+        with cuda.device(dev):
+            st = f(*args, (cuda.current_stream() if stream is None else stream).cuda_stream)
+    check(fn, st)
 
 
 # ---- position rotation and per-head norms ----------------------------------
@@ -78,24 +96,31 @@ def make_rope(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor
     return r
 
 
-def _rows(on, x, out, weight, name, head_first, dim):
-    """The Rows struct of one side: x [B, T, H, D] with any batch, token and head strides."""
+def _rows(x, out, weight, name, dev, ref, head_first):
+    """The tq_rows of one side, x [B, T, heads, D] with any batch, token and head
+    strides; ref: (batch, tokens, D, dtype, output dtype) of the call."""
     if x is None:
         if out is not None:
             raise ValueError(f"{name}_out without {name}")
         return None
-    if x.dim() != 4 or x.shape[3] != dim or (x.stride(3) != 1 and dim > 1):
-        raise ValueError(f"{name} must be [B, T, heads, head_dim] with contiguous rows")
-    b, t, h, _ = x.shape
-    want = (b, h, t, dim) if head_first else (b, t, h, dim)
-    if out is None or tuple(out.shape) != want:
-        raise ValueError(f"{name}_out must have shape {want}")
-    if weight is not None and tuple(weight.shape) != (dim,):
-        raise ValueError(f"{name}_weight must have shape ({dim},)")
-    # a stride of a dimension of one element says nothing
-    s = [x.stride(i) if x.shape[i] > 1 else 0 for i in range(3)]
-    return Rows(on.ptr(x, name, contiguous=False), on.ptr(out, name + "_out"), on.ptr(weight, name + "_weight"), h,
-                s[0], s[1], s[2])
+    if x.dim() != 4:
+        raise ValueError(f"{name} must be [B, T, heads, head_dim]")
+    b, t, h, d = x.shape
+    sb, st, sh, sd = x.stride()
+    batch, tokens, dim, dtype, out_dtype = ref
+    if b != batch or t != tokens or d != dim or x.dtype is not dtype:
+        raise ValueError("q, k and v must have the same batch, tokens, head_dim and dtype")
+    if sd != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    want = (b, h, t, d) if head_first else (b, t, h, d)
+    if out is None or out.shape != want or out.dtype is not out_dtype:
+        raise ValueError(f"{name}_out must have shape {want}, all outputs one dtype")
+    if weight is not None and weight.shape != (d,):
+        raise ValueError(f"{name}_weight must have shape ({d},)")
+    # the stride of a dimension of one element says nothing
+    return _ROWS.pack(_ptr(x, name, dev, False), _ptr(out, name + "_out", dev),
+                      _ptr(weight, name + "_weight", dev) or 0, h, sb if b > 1 else 0, st if t > 1 else 0,
+                      sh if h > 1 else 0)
 
 
 def qk_norm_rope(rope: Rope | None, q=None, k=None, v=None, positions=None, q_out=None, k_out=None, v_out=None,
@@ -106,28 +131,24 @@ def qk_norm_rope(rope: Rope | None, q=None, k=None, v=None, positions=None, q_ou
     q, k, v: [B, T, heads, D], any strides with contiguous rows (a split of a
     joint projection), one dtype; positions: int32 [B, T].  q_out: [B, T, Hq, D];
     k_out, v_out: [B, Hkv, T, D], as encode_kv takes them."""
-    given = [(n, x, o) for n, x, o in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)) if x is not None]
-    if not given:
-        raise ValueError("q, k or v is required")
-    name, first, out0 = given[0]
-    on = _On(first, name)
+    first, out0 = (q, q_out) if q is not None else (k, k_out) if k is not None else (v, v_out)
+    if first is None or out0 is None:
+        raise ValueError("q, k or v is required, with its output")
+    dev = _device(first, "q" if q is not None else "k" if k is not None else "v")
     if first.dim() != 4:
-        raise ValueError(f"{name} must be [B, T, heads, head_dim]")
-    b, t, _, dim = first.shape
-    for n, x, o in given:
-        if tuple(x.shape[:2]) != (b, t) or x.dtype != first.dtype:
-            raise ValueError("q, k and v must have the same batch, tokens and dtype")
-        if o is None or o.dtype != out0.dtype:
-            raise ValueError(f"{n}_out is required, all outputs of one dtype")
-    weights = [w for w in (q_weight, k_weight) if w is not None]
-    if any(w.dtype != weights[0].dtype for w in weights):
-        raise ValueError("q_weight and k_weight must have the same dtype")
-    sides = [_rows(on, q, q_out, q_weight, "q", False, dim), _rows(on, k, k_out, k_weight, "k", True, dim),
-             _rows(on, v, v_out, None, "v", True, dim)]
-    on.call("tq_qk_norm_rope", stream, None if rope is None else ctypes.byref(rope), b, t, dim,
-            *(None if s is None else ctypes.byref(s) for s in sides), _code(first.dtype),
-            _code(weights[0].dtype) if weights else TQ_F32, _code(out0.dtype), int(norm), eps, weight_bias,
-            on.i32(positions, "positions", (b, t)), on.i32(n_tok, "n_tok", (b,)))
+        raise ValueError("q, k and v must be [B, T, heads, head_dim]")
+    b, t, _, d = first.shape
+    ref = (b, t, d, first.dtype, out0.dtype)
+    w_dtype = TQ_F32
+    if q_weight is not None or k_weight is not None:
+        w = q_weight if q_weight is not None else k_weight
+        if k_weight is not None and k_weight.dtype is not w.dtype:
+            raise ValueError("q_weight and k_weight must have the same dtype")
+        w_dtype = _code(w.dtype)
+    _call("tq_qk_norm_rope", dev, stream, None if rope is None else ctypes.byref(rope), b, t, d,
+          _rows(q, q_out, q_weight, "q", dev, ref, False), _rows(k, k_out, k_weight, "k", dev, ref, True),
+          _rows(v, v_out, None, "v", dev, ref, True), _code(first.dtype), w_dtype, _code(out0.dtype), 1 if norm else 0,
+          eps, weight_bias, _i32(positions, "positions", dev, (b, t)), _i32(n_tok, "n_tok", dev, (b,)))
 
 
 # ---- attention of a tree of drafted tokens ----------------------------------
@@ -158,37 +179,37 @@ def alloc_tree_workspace(desc: KVDesc, q_heads: int, n_q: int, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _cache_ptrs(on, cache: Cache):
-    return [on.ptr(getattr(cache, n), n) for n in ("k_codes", "k_norms", "v_codes", "v_norms")]
-
-
 def decode_attention_tree(cache: Cache, k_cb: Codebook, v_cb: Codebook, q, seq_lens, tree, scale: float, out, workspace,
                           n_nodes=None, status=None, stream=None):
     """Attention of a tree of drafted tokens over the packed cache
     (tq_decode_attention_tree).  q, out: [B, n_q, Hq, D] (out fp16 or bf16);
     tree: int64 [B, n_q] ancestor masks; the last n_nodes[b] (default n_q) of
     seq_lens[b] cached positions are the drafted nodes."""
-    on = _On(q, "q")
+    dev = _device(q, "q")
     if q.dim() != 4 or out.shape != q.shape:
         raise ValueError("q and out must be [B, n_q, heads, head_dim], of one shape")
     b, n_q, heads, dim = q.shape
-    if (b, dim) != (cache.desc.batch, cache.desc.head_dim):
+    desc = cache.desc
+    if b != desc.batch or dim != desc.head_dim:
         raise ValueError("q does not match the cache's batch and head_dim")
-    import torch
-    if tree.dtype not in (torch.int64, torch.uint64) or tuple(tree.shape) != (b, n_q):
+    if tree.element_size() != 8 or tree.is_floating_point() or tree.shape != (b, n_q):
         raise ValueError(f"tree must be int64 of shape {(b, n_q)}")
-    on.call("tq_decode_attention_tree", stream, ctypes.byref(cache.desc), ctypes.byref(k_cb), ctypes.byref(v_cb), heads,
-            n_q, on.ptr(q, "q"), _code(q.dtype), *_cache_ptrs(on, cache), on.i32(seq_lens, "seq_lens", (b,)),
-            on.i32(n_nodes, "n_nodes", (b,)), on.ptr(tree, "tree"), scale, on.ptr(out, "out"), _code(out.dtype),
-            on.ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), on.ptr(status, "status"))
+    _call("tq_decode_attention_tree", dev, stream, ctypes.byref(desc), ctypes.byref(k_cb), ctypes.byref(v_cb), heads,
+          n_q, _ptr(q, "q", dev), _code(q.dtype), _ptr(cache.k_codes, "k_codes", dev),
+          _ptr(cache.k_norms, "k_norms", dev), _ptr(cache.v_codes, "v_codes", dev),
+          _ptr(cache.v_norms, "v_norms", dev), _i32(seq_lens, "seq_lens", dev, (b,)),
+          _i32(n_nodes, "n_nodes", dev, (b,)), _ptr(tree, "tree", dev), scale, _ptr(out, "out", dev),
+          _code(out.dtype), _ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
+          _status(status, dev))
     return out
 
 
 # ---- rows of the cache -------------------------------------------------------
 
-def _bufs(on, cache: Cache, vo: VOutliers | None) -> CacheBufs:
-    return CacheBufs(*_cache_ptrs(on, cache), None if vo is None else on.ptr(vo.values, "values"),
-                     0 if vo is None else vo.k)
+def _bufs(cache: Cache, vo: VOutliers | None, dev) -> CacheBufs:
+    return CacheBufs(_ptr(cache.k_codes, "k_codes", dev), _ptr(cache.k_norms, "k_norms", dev),
+                     _ptr(cache.v_codes, "v_codes", dev), _ptr(cache.v_norms, "v_norms", dev),
+                     None if vo is None else _ptr(vo.values, "values", dev), 0 if vo is None else vo.k)
 
 
 def cache_compact(cache: Cache, keep, n_keep, start=None, new_lens=None, vo: VOutliers | None = None, status=None,
@@ -196,25 +217,29 @@ def cache_compact(cache: Cache, keep, n_keep, start=None, new_lens=None, vo: VOu
     """Keep chosen rows of every sequence, in place (tq_cache_compact): row
     keep[b, i] becomes row start[b] + i for i < n_keep[b].  keep: int32
     [B, max_keep]; vo: the side data of a v3 cache."""
-    on = _On(cache.k_codes, "k_codes")
+    dev = _device(cache.k_codes, "k_codes")
     b = cache.desc.batch
     if keep.dim() != 2:
         raise ValueError("keep must be [B, max_keep]")
-    on.call("tq_cache_compact", stream, ctypes.byref(cache.desc), ctypes.byref(_bufs(on, cache, vo)),
-            on.i32(keep, "keep", (b, keep.shape[1])), keep.shape[1], on.i32(n_keep, "n_keep", (b,)),
-            on.i32(start, "start", (b,)), on.i32(new_lens, "new_lens", (b,)), on.ptr(status, "status"))
+    m = keep.shape[1]
+    _call("tq_cache_compact", dev, stream, ctypes.byref(cache.desc), ctypes.byref(_bufs(cache, vo, dev)),
+          _i32(keep, "keep", dev, (b, m)), m, _i32(n_keep, "n_keep", dev, (b,)), _i32(start, "start", dev, (b,)),
+          _i32(new_lens, "new_lens", dev, (b,)), _status(status, dev))
 
 
 def cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, n_rows, max_rows: int, src_pos=None, dst_pos=None,
                src_vo: VOutliers | None = None, dst_vo: VOutliers | None = None, status=None, stream=None) -> None:
     """Copy row ranges between cache slots (tq_cache_copy): n_rows[c] rows from
     src_pos[c] of slot src_slot[c] to dst_pos[c] of slot dst_slot[c]."""
-    on = _On(src.k_codes, "k_codes")
+    dev = _device(src.k_codes, "k_codes")
     n = src_slot.shape[0]
-    on.call("tq_cache_copy", stream, ctypes.byref(src.desc), ctypes.byref(_bufs(on, src, src_vo)),
-            ctypes.byref(dst.desc), ctypes.byref(_bufs(on, dst, dst_vo)), n, on.i32(src_slot, "src_slot", (n,)),
-            on.i32(dst_slot, "dst_slot", (n,)), on.i32(src_pos, "src_pos", (n,)), on.i32(dst_pos, "dst_pos", (n,)),
-            on.i32(n_rows, "n_rows", (n,)), max_rows, on.ptr(status, "status"))
+    shape = (n,)
+    a = ctypes.byref(_bufs(src, src_vo, dev))
+    b = a if dst is src and dst_vo is src_vo else ctypes.byref(_bufs(dst, dst_vo, dev))
+    _call("tq_cache_copy", dev, stream, ctypes.byref(src.desc), a, ctypes.byref(dst.desc), b, n,
+          _i32(src_slot, "src_slot", dev, shape), _i32(dst_slot, "dst_slot", dev, shape),
+          _i32(src_pos, "src_pos", dev, shape), _i32(dst_pos, "dst_pos", dev, shape),
+          _i32(n_rows, "n_rows", dev, shape), max_rows, _status(status, dev))
 
 
 __all__ = ["TQ_MAX_TREE_NODES", "alloc_tree_workspace", "cache_compact", "cache_copy", "decode_attention_tree",
