@@ -160,6 +160,7 @@ size_t tq_tree_workspace_size(const tq_kv_desc* desc, int q_heads, int n_q) {
   if (desc->head_dim > tq::kMaxDecodeHeadDim || desc->batch > tq::kMaxBatch) return 0;
   if (q_heads < desc->kv_heads || q_heads % desc->kv_heads != 0) return 0;
   if (n_q < 1 || n_q > TQ_MAX_TREE_NODES) return 0;
+  if ((long long)desc->batch * q_heads * n_q >= (1LL << 31)) return 0;
   return tq::tree_workspace_bytes(desc->batch, desc->kv_heads, q_heads, desc->head_dim, n_q);
 }
 
@@ -176,7 +177,7 @@ int tq_decode_attention_tree(const tq_kv_desc* desc, const tq_codebook* k_cb, co
                                seq_lens, scale, 0.0f, static_cast<const float*>(out), dev_status);
   if (st != TQ_OK) return st;
   if (!tree || !aligned(tree, 8) || !aligned(n_nodes, 4)) return TQ_ERR_INVALID_ARG;
-  if ((long long)desc->kv_heads * q_heads >= (1 << 24)) return TQ_ERR_UNSUPPORTED;
+  if ((long long)desc->batch * q_heads * n_q >= (1LL << 31)) return TQ_ERR_UNSUPPORTED;
   const size_t need = tq_tree_workspace_size(desc, q_heads, n_q);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return TQ_ERR_WORKSPACE;
   tq::TreeParams p{};

@@ -564,7 +564,10 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
     uint32_t dyn;
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
     if (smem_u32(smem) != kBase || dyn < pl.bytes) {  // another layout of the shared window: reported, never used
-      if (tid == 0 && p.status) atomicOr(p.status, TQ_DEV_INTERNAL);
+      if (tid == 0) {
+        if (p.status) atomicOr(p.status, TQ_DEV_INTERNAL);
+        P.ws_join[blockIdx.x] = Join{};
+      }
       return;
     }
   }
@@ -1453,13 +1456,6 @@ bool plan(const TreeParams& p, Plan& pl) {
   return false;
 }
 
-int sm_count(int* out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
-  if (cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return TQ_ERR_CUDA;
-  return TQ_OK;
-}
-
 template <int NB, int N>
 int run(Params& P, cudaStream_t stream) {
   const TreeParams& p = P.t;
@@ -1468,9 +1464,22 @@ int run(Params& P, cudaStream_t stream) {
   P.group = FastDiv::make((uint32_t)(p.q_heads / p.kv_heads));
   const long long tiles =
       (long long)p.batch * p.kv_heads * P.n_hg * ((p.seq_cap + kTok - 1) / kTok);
-  int sms = 0;
-  if (sm_count(&sms) != TQ_OK) return TQ_ERR_CUDA;
-  const int grid = (int)min(min((long long)sms, (long long)kMaxGrid), tiles);
+  // set up once per device
+  auto kern = tree_kernel<NB, N>;
+  static int sm_counts[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return TQ_ERR_CUDA;
+  if (sm_counts[dev] == 0) {
+    int sms = 0;
+    cudaFuncAttributes attrs;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn) != cudaSuccess ||
+        cudaFuncGetAttributes(&attrs, kern) != cudaSuccess)
+      return TQ_ERR_CUDA;
+    if (attrs.numRegs < Roles<N>::kLaunch) return TQ_ERR_UNSUPPORTED;  // the register split would never be granted
+    sm_counts[dev] = sms;
+  }
+  const int grid = (int)min(min((long long)sm_counts[dev], (long long)kMaxGrid), tiles);
   char* ws = static_cast<char*>(p.workspace);
   const size_t units = (size_t)p.batch * p.kv_heads * P.n_hg;
   P.ws_mul = reinterpret_cast<float*>(ws);
@@ -1482,12 +1491,6 @@ int run(Params& P, cudaStream_t stream) {
   P.ws_acc = reinterpret_cast<float*>(ws);
   ws += (size_t)2 * kMaxGrid * N * NB * kBlock * 4;
   P.ws_q = reinterpret_cast<uint8_t*>(ws);
-  auto kern = tree_kernel<NB, N>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn) != cudaSuccess)
-    return TQ_ERR_CUDA;
-  cudaFuncAttributes attr_k;
-  if (cudaFuncGetAttributes(&attr_k, kern) != cudaSuccess) return TQ_ERR_CUDA;
-  if (attr_k.numRegs < Roles<N>::kLaunch) return TQ_ERR_UNSUPPORTED;  // the register split would never be granted
   // The kernel's set-up runs beside the query kernel, the join kernel's launch
   // beside the kernel's end (programmatic dependent launches).
   query_kernel<NB, N><<<(unsigned)units, 512, 0, stream>>>(P);
