@@ -412,7 +412,14 @@ __device__ __forceinline__ uint32_t pair_addr(const uint32_t* w, int q, uint32_t
   return (x & (((1u << (2 * B)) - 1u) << 7)) | lane_base;
 }
 
-// Codes of 2 or 3 bits without a table in shared memory: eight codes are spread
+// Whether K codes go through a table in shared memory.  Byte permutes take no
+// shared-memory bandwidth but a third more instructions: for heads of one
+// block they win where that bandwidth binds (rows of 16 to 64 columns: 130,
+// 137, 166 us against 136, 143, 171 on 8 x 32768 positions of 3 + 3 bits), for
+// heads of two the K warps bind (291 against 249 us, 256-wide heads, 3 + 2 bits).
+__host__ __device__ constexpr bool k_table(int nb, int bits) { return bits == 4 || nb == 2; }
+
+// Codes of 2 or 3 bits without a table: eight codes are spread
 // to one per nibble (x + (x & high) * (2^s - 1) moves the high half up by s), a
 // byte permute picks the low bytes of four levels and another the high bytes,
 // and two more interleave them to fp16 pairs.
@@ -463,12 +470,12 @@ __device__ __forceinline__ void expand_to_smem(const uint32_t (&w)[4 * B], uint3
   }
 }
 // Their values as 64 columns of this lane's row of tensor memory.
-template <int B>
+template <int B, bool TABLE>
 __device__ __forceinline__ void expand_to_tmem(const uint32_t (&w)[4 * B], uint32_t addr, uint32_t lane_base, const Levels& lv) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t v[16];
-    if constexpr (B == 4) {
+    if constexpr (TABLE) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = lds_table(pair_addr<B>(w, 16 * c + i, lane_base));
     } else {
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       *reinterpret_cast<__half2*>(gen(base + 4u * (uint32_t)e)) = h;
     }
   };
-  if (p.k_bits == 4 && pl.lut_k != pl.lut_v) fill(p.k_bits, p.kcent, P.kscale, pl.lut_k);
+  if (k_table(NB, p.k_bits) && pl.lut_k != pl.lut_v) fill(p.k_bits, p.kcent, P.kscale, pl.lut_k);
   fill(p.v_bits, p.vcent, P.vscale, pl.lut_v);
   bool empty = false;
   if (tid < 512) {
@@ -1010,7 +1017,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
                 }
                 if (i + 1 < tiles) fetch_norms(i + 1);
               }
-              expand_to_tmem<B>(w, tm_k + stage * 64, lane_base, P.klev);
+              expand_to_tmem<B, k_table(NB, B)>(w, tm_k + stage * 64, lane_base, P.klev);
               tc_before();
             }
             __syncwarp();
@@ -1436,10 +1443,10 @@ bool plan(const TreeParams& p, Plan& pl) {
     pl.v_stages = t[0];
     pl.p_stages = t[1];
     pl.depth = t[2];
-    // tables: V's, and K's for 4-bit codes, one for both where the levels are
+    // tables: V's, and K's where it has one, one for both where the levels are
     pl.lut_v = take(128u << (2 * p.v_bits), 128u << (2 * p.v_bits));
-    if (p.k_bits == 4) {
-      const bool same = p.v_bits == 4 && memcmp(p.kcent, p.vcent, sizeof(p.kcent)) == 0;
+    if (k_table(NB, p.k_bits)) {
+      const bool same = p.v_bits == p.k_bits && memcmp(p.kcent, p.vcent, sizeof(p.kcent)) == 0;
       pl.lut_k = same ? pl.lut_v : take(128u << (2 * p.k_bits), 128u << (2 * p.k_bits));
     }
     pl.vt = take(2 * kPanel * t[0], 1024);
