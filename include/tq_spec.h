@@ -135,7 +135,8 @@ size_t tq_tree_workspace_size(const tq_kv_desc* desc, int q_heads, int n_q);
  *   - Values in positions that a row does not see (infinite or NaN norms
  *     included) do not reach it.
  *   - workspace: tq_tree_workspace_size() bytes, 256-byte aligned, any
- *     content; calls that share one must not overlap in time.
+ *     content; calls that share one must not overlap in time.  Three launches
+ *     (queries, attention, join), the last two as programmatic dependents.
  * seq_lens, limits and errors otherwise as tq_decode_attention (head_dim 128
  * or 256, even seq_cap, batch <= 2048, any q_heads / kv_heads ratio).
  */
@@ -172,7 +173,8 @@ typedef struct {
  *     negative start skips the sequence (TQ_DEV_POS_RANGE).
  *   - new_lens: device int32 [batch] or NULL; gets start[b] + n_keep[b]
  *     (clamped to [0, seq_cap]).  May be the seq_lens array of the decode
- *     calls that follow on the stream.
+ *     calls that follow on the stream, but none of the arrays above
+ *     (TQ_ERR_INVALID_ARG where they overlap).
  * max_keep == 0 is a no-op apart from new_lens.  head_dim up to 512.
  */
 int tq_cache_compact(const tq_kv_desc* desc, const tq_cache_bufs* cache, const int32_t* keep,

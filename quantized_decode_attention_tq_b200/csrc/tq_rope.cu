@@ -343,13 +343,14 @@ rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastD
 
 template <int IN, int OUT, int LPR, int MODE>
 int run_rope(const RopeParams& p, cudaStream_t stream) {
-  // One token per CTA while that gives every SM no more than four CTAs, then
-  // more: the tables are filled by all threads at once.
+  // One token per CTA, and more while that leaves every SM sixteen CTAs: the
+  // tables are filled by all threads at once, but a last wave of few CTAs
+  // costs more (4004 tokens of 24 rows: 35 us at eight tokens a CTA).
   constexpr int kGroups = kRopeThreads / LPR;
   const int D = p.head_dim, pitch = MODE == kAnyHalves ? D / 2 + D / 32 : D / 2;
   const long long tokens = (long long)p.batch * p.seq_new;
   int TT = 1;
-  while (TT < kMaxTT && tokens > (long long)TT * 4 * 148) TT *= 2;
+  while (TT < kMaxTT && tokens > (long long)TT * 16 * 148) TT *= 2;
   const size_t smem = sizeof(float) * ((size_t)2 * TT * pitch + 2 * D + (MODE == kAnyHalves ? kGroups * (D + D / 16) : 0));
   rope_kernel<IN, OUT, LPR, MODE><<<(unsigned)((tokens + TT - 1) / TT), kRopeThreads, smem, stream>>>(
       p, TT, FastDiv::make((uint32_t)p.rows), FastDiv::make((uint32_t)p.seq_new));

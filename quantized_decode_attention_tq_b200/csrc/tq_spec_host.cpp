@@ -11,6 +11,11 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+bool overlap(const void* a, size_t n, const void* b, size_t m) {  // of two given ranges
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + m && y < x + n;
+}
+
 bool valid_dtype(int t) { return t == TQ_F32 || t == TQ_F16 || t == TQ_BF16; }
 size_t dtype_size(int t) { return t == TQ_F32 ? 4 : 2; }
 
@@ -220,6 +225,11 @@ int tq_cache_compact(const tq_kv_desc* desc, const tq_cache_bufs* cache, const i
   if (max_keep < 0 || !n_keep || (max_keep > 0 && !keep)) return TQ_ERR_INVALID_ARG;
   if (!aligned(keep, 4) || !aligned(n_keep, 4) || !aligned(start, 4) || !aligned(new_lens, 4) ||
       !aligned(dev_status, 4))
+    return TQ_ERR_INVALID_ARG;
+  // new_lens is written while other CTAs still read the lists
+  const size_t per_seq = sizeof(int32_t) * (size_t)desc->batch;
+  if (overlap(new_lens, per_seq, start, per_seq) || overlap(new_lens, per_seq, n_keep, per_seq) ||
+      overlap(new_lens, per_seq, keep, per_seq * (size_t)max_keep))
     return TQ_ERR_INVALID_ARG;
   if ((long long)desc->batch * desc->kv_heads >= (1LL << 27)) return TQ_ERR_UNSUPPORTED;
   if (max_keep == 0 && !new_lens) return TQ_OK;

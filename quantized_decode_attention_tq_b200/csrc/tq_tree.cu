@@ -26,7 +26,11 @@
 // (two MMAs), the centroids are scaled by a factor that makes their rounding
 // small (centroid_scale), and weight * norm is rounded once.
 //
-// Warps: see Roles.
+// What it measured (a pass, one B200): trees of 16 nodes on 8 x 32768 positions
+// of 3 + 3 bits 166 us, 64 nodes on 131072 of 4 + 2 bits 272 us; a tile of 64
+// columns about 2500 cycles, with 62% of the issue slots and some 90% of the
+// shared-memory bandwidth taken (7000 instructions: 1300 for K, 930 for V, the
+// softmax most of the rest).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,11 +45,15 @@ namespace tq {
 namespace tree {
 namespace {
 
-constexpr int kTok = 128;           // positions per tile
+constexpr int kTok = 128;  // positions per tile
+
 // Roles by warpgroup (four warps): softmax groups of 128 threads, each with its
 // share of the row group's columns; one group that turns K codes into fp16 and
-// one for V; one whose warps issue the score MMAs, the V MMAs and the copies.  Registers per thread
-// at launch, then by role: the shares must fit the launch's total.
+// one for V; one whose warps issue the score MMAs, the V MMAs and the copies.
+// Four softmax groups from 64 columns on: with two, 64 columns took 198 us
+// where four take 188 (8 x 32768 positions).  Registers per thread at launch,
+// then by role; the shares must fit the launch's total.  At four groups 80, 64
+// and 56 leave 64 columns without spills (other splits: 3 to 25% slower).
 template <int N>
 struct Roles {
   static constexpr int kGroups = N >= 64 ? 4 : 2;
@@ -55,12 +63,17 @@ struct Roles {
   static constexpr int kSoft = kGroups == 4 ? 80 : 136, kCodes = kGroups == 4 ? 64 : 72, kMma = kGroups == 4 ? 56 : 64;
   static_assert(kGroups * kSoft + 2 * kCodes + kMma <= (kWarps / 4) * kLaunch, "register split");
 };
+
 constexpr int kMaxGrid = 256;       // CTAs at most (slots of the workspace)
 constexpr uint32_t kBase = 1024;    // shared-window address of dynamic shared memory
 constexpr uint32_t kMaxDyn = 227 * 1024;
 constexpr float kTau = 6.0f;        // log2: how far a score may exceed the reference maximum
 constexpr float kUnset = -1e30f;    // reference of a row that has seen no position
-constexpr float kNormRoom = 512.0f; // V norms up to 2^9 times the unit's scale: 2^(6+9) fits fp16
+// V norms are scaled by a power of two that puts the largest one seen when it
+// is chosen at 2^7: norms down to 2^-21 of it keep full fp16 precision at weight
+// 1, and the scale is chosen anew when one exceeds 2^9 (2^(6 + 9) fits fp16).
+constexpr int kNormTop = 7;
+constexpr float kNormRoom = 512.0f;
 constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element x 128-row panel
 
 struct Plan {
@@ -80,7 +93,7 @@ struct Levels {
 // What the join kernel needs of the unit that a CTA's range starts inside of:
 // parts first - 1 .. last (of the split) hold it.
 struct Join {
-  int b, kvh, hg, first, last;  // first = 0: the CTA's range starts with a unit, or the cut was not its first
+  int b, kvh, hg, first, last, nodes;  // first = 0: the CTA's range starts with a unit, or the cut was not its first
 };
 
 struct Params {
@@ -361,18 +374,43 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
-// The flattened tiles [0, T) are cut into `parts` ranges of equal size.
+// The flattened tiles [0, total) are cut into `parts` ranges of equal cost: a
+// tile costs 1, and the end of a unit kSwitch more (the partial, the next
+// unit's query and the references of its first tile).  A tree of 64 nodes on
+// 131072 positions: 277 us with no such cost, 272 with 3, 5 or 8; other cases
+// within 1%.  With few tiles per part the boundary counts nothing, so that no
+// range is empty.
+constexpr int kSwitch = 3;
 struct Cut {
   const int* prefix;  // tiles before each batch entry
   int batch, ub;      // ub: units per batch entry
-  long long total, parts;
+  long long total, parts, sw, cost;
   __device__ Cut(const int* pre, int b, int units, int grid) : prefix(pre), batch(b), ub(units) {
     total = (long long)pre[b] * units;
     parts = min((long long)grid, total);
+    sw = total >= 4LL * kSwitch * grid ? kSwitch : 0;
+    cost = total + sw * units * (long long)b;
   }
-  __device__ long long start(long long c) const { return c >= parts ? total : quotient(c * total, parts); }
-  // the part that holds tile x
-  __device__ long long part_of(long long x) const { return quotient((x + 1) * parts - 1, total); }
+  __device__ long long before(int b) const { return (long long)ub * (prefix[b] + sw * b); }  // cost of the entries before b
+  // first tile of part c
+  __device__ long long start(long long c) const {
+    if (c >= parts) return total;
+    const long long y = quotient(c * cost, parts);
+    if (sw == 0) return y;
+    int lo = 0, hi = batch;  // the last entry whose cost starts at or before y
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) <= y) lo = mid;
+      else hi = mid;
+    }
+    const long long nt = prefix[lo + 1] - prefix[lo], rest = y - before(lo), r = quotient(rest, nt + sw);
+    return (long long)ub * prefix[lo] + r * nt + min(rest - r * (nt + sw), nt);
+  }
+  // the part that holds tile t of unit r of batch entry b
+  __device__ long long part_of(int b, int r, int t) const {
+    const long long nt = prefix[b + 1] - prefix[b];
+    return quotient((before(b) + r * (nt + sw) + t + 1) * parts - 1, cost);
+  }
 };
 
 struct Seg {
@@ -814,7 +852,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
 #pragma unroll
               for (int w = 0; w < 4; ++w) vm = fmaxf(vm, miscf[M::kVmax + 4 * grp + w]);
               if (vm > 0.0f && (tile == sg.lo || vm * vpow > kNormRoom)) {
-                const float np = ldexpf(1.0f, -ilogbf(vm));
+                const float np = ldexpf(1.0f, kNormTop - ilogbf(vm));
                 beta = np / vpow;
                 vpow = np;
                 grown = true;
@@ -1156,8 +1194,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       Join j{};
       if (begin < end) {
         const Seg sg = find(cut, begin, end, P.n_hg);
-        if (sg.lo > 0 && cut.part_of(sg.begin) == (long long)blockIdx.x - 1)
-          j = Join{sg.b, sg.kvh, sg.hg, (int)blockIdx.x, (int)cut.part_of(sg.begin + sg.nt - 1)};
+        if (sg.lo > 0 && cut.part_of(sg.b, sg.r, 0) == (long long)blockIdx.x - 1)
+          j = Join{sg.b, sg.kvh, sg.hg, (int)blockIdx.x, (int)cut.part_of(sg.b, sg.r, sg.nt - 1), clamp_nodes(p, sg.b)};
       }
       P.ws_join[blockIdx.x] = j;
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1291,7 +1329,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
   if (jn.first == 0) return;
   const int vl = jn.hg * N + n;
   if (vl >= (int)P.group.d * p.n_q) return;
-  const long long row = out_row(P, jn.b, jn.kvh, vl, clamp_nodes(p, jn.b));
+  const long long row = out_row(P, jn.b, jn.kvh, vl, jn.nodes);
   if (row < 0) return;
   // part c - 1 holds the unit's first tiles (its last segment: slot 2 (c-1) + 1),
   // parts c, c + 1, ... the rest (their first segments: slots 2 c', ...)

@@ -237,6 +237,16 @@ def test_tree_norms_that_grow_along_the_sequence():
     _tree_case(5, 1, 4, 1, 128, 3, 3, 900, [900], 4, cache=cache, dst="bfloat16")
 
 
+def test_tree_small_values_behind_large_ones_of_no_weight():
+    """The first 128 positions hold V 2^17 times larger than the rest, at weights
+    around e^-15 of theirs: the sum is that of the small ones."""
+    rng = np.random.default_rng(17)
+    cache = R.random_cache(rng, 1, 1, 700, 128, 4, 4)
+    cache[1][0, 0, :, 0], cache[1][0, 0, :128, 0] = 60.0, 0.5
+    cache[3][0, 0, :, 0], cache[3][0, 0, :128, 0] = 0.015, 2000.0
+    _tree_case(6, 1, 4, 1, 128, 4, 4, 700, [700], 4, cache=cache, dst="bfloat16")
+
+
 @pytest.mark.parametrize("bad", [np.inf, np.nan])
 def test_tree_hidden_values_do_not_reach_a_row(bad):
     torch = torch_mod()
@@ -296,6 +306,13 @@ def test_tree_many_uneven_sequences():
     _tree_case(14, 37, 4, 2, 128, 2, 3, 400, lens, 3, counts=counts, sign_seed=77)
 
 
+def test_tree_long_uneven_sequences_cut_between_units():
+    # enough 128-position tiles (1856) for cuts that weigh the units' ends, an
+    # empty sequence among them
+    lens = [10000, 0, 9130, 3001, 7200]
+    _tree_case(21, 5, 8, 8, 128, 3, 3, 10000, lens, 2, counts=[2, 0, 1, 2, 2])
+
+
 def test_tree_lengths_out_of_range_are_clamped():
     torch = torch_mod()
     rng = np.random.default_rng(15)
@@ -346,6 +363,32 @@ def test_tree_repeats_bit_for_bit_and_replays_in_a_graph():
     torch.cuda.synchronize()
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+def test_tree_calls_at_once_on_two_streams():
+    torch = torch_mod()
+    rng = np.random.default_rng(18)
+    cache = R.random_cache(rng, 2, 2, 2000, 128, 3, 3)
+    desc = tq.kv_desc(2, 2, 128, 2000, 3, 3)
+    dc, cb = _dev_cache(cache, desc), tq.make_codebook(3)
+    lens = to_dev(np.array([2000, 1777], dtype=np.int32))
+    masks = to_dev(np.stack([_random_tree(rng, 5) for _ in range(2)]))
+    qs = [torch.randn(2, 5, 8, 128, device="cuda", dtype=torch.float16) for _ in range(2)]
+    wss = [tq.alloc_tree_workspace(desc, 8, 5) for _ in range(2)]
+    want = []
+    for q in qs:
+        o = torch.zeros_like(q)
+        tq.decode_attention_tree(dc, cb, cb, q, lens, masks, 0.0884, o, wss[0])
+        want.append(o)
+    outs = [torch.zeros_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, ws, o, s in zip(qs, wss, outs, streams):
+            tq.decode_attention_tree(dc, cb, cb, q, lens, masks, 0.0884, o, ws, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
 
 
 # --------------------------------------------------------------- cache rows --

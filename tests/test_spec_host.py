@@ -152,6 +152,9 @@ def test_compact_refusals():
     assert call(keep=None) == BAD and call(n=None) == BAD and call(m=-1) == BAD
     assert call(keep=GOOD + 1) == BAD and call(n=GOOD + 2) == BAD and call(start=GOOD + 2) == BAD
     assert call(lens=GOOD + 2) == BAD
+    far = GOOD + (1 << 20)
+    assert call(start=far, lens=far) == BAD and call(n=far, lens=far + 4) == BAD  # written while they are read
+    assert call(keep=far, lens=far + 28) == BAD and call(m=0, n=far, lens=far - 4) == BAD
 
 
 def test_copy_refusals():
