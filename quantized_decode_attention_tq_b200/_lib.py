@@ -99,7 +99,8 @@ SIGNATURES = {
     "tq_status_string": (ctypes.c_char_p, [c_int]),
 }
 
-# Every symbol include/tq_spec.h declares.
+# Every symbol include/tq_spec.h declares.  tq_rows and tq_cache_bufs pass as
+# packed bytes (spec.py) or as the structures above.
 c_double = ctypes.c_double
 SPEC_SIGNATURES = {
     "tq_make_rope": (c_int, [c_int, c_int, c_double, c_int, c_double, c_double, c_double, c_double, _P(Rope)]),
@@ -110,9 +111,9 @@ SPEC_SIGNATURES = {
     "tq_decode_attention_tree": (c_int, [_P(KVDesc), _P(Codebook), _P(Codebook), c_int, c_int, c_void_p, c_int,
                                          c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_float, c_void_p, c_int, c_void_p, c_size_t, c_void_p, c_void_p]),
-    "tq_cache_compact": (c_int, [_P(KVDesc), _P(CacheBufs), c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+    "tq_cache_compact": (c_int, [_P(KVDesc), c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p]),
-    "tq_cache_copy": (c_int, [_P(KVDesc), _P(CacheBufs), _P(KVDesc), _P(CacheBufs), c_int, c_void_p, c_void_p,
+    "tq_cache_copy": (c_int, [_P(KVDesc), c_void_p, _P(KVDesc), c_void_p, c_int, c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p]),
 }
 

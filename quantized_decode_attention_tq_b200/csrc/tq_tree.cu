@@ -14,8 +14,8 @@
 // thread owns one position (its two norms are registers), and both operands
 // made from codes are written in the cache's own order: K^ as rows of tensor
 // memory, V^ as M-major and P as N-major rows of shared memory, 128-byte
-// swizzled.  Shared-memory bandwidth is what runs out first (table lookups, V^
-// and P in and out), so K^ does not pass through it.
+// swizzled.  Shared-memory bandwidth ran out first (table lookups, V^ and P in
+// and out: 96% taken with K^ there too), so K^ does not pass through it.
 //
 // Softmax in the log2 domain with a lazy reference maximum per row: a tile is
 // scored against it, and only when some score exceeds it by 2^kTau do the
@@ -27,10 +27,11 @@
 // small (centroid_scale), and weight * norm is rounded once.
 //
 // What it measured (a pass, one B200): trees of 16 nodes on 8 x 32768 positions
-// of 3 + 3 bits 166 us, 64 nodes on 131072 of 4 + 2 bits 272 us; a tile of 64
-// columns about 2500 cycles, with 62% of the issue slots and some 90% of the
-// shared-memory bandwidth taken (7000 instructions: 1300 for K, 930 for V, the
-// softmax most of the rest).
+// of 3 + 3 bits 166 us, 64 nodes on 131072 of 4 + 2 bits 272 us.  A tile of 64
+// columns takes about 2500 cycles and 6500 warp instructions (1300 for K, 930
+// for V, 3600 in the softmax) with 58% of the issue slots, 61% of the
+// shared-memory bandwidth and 24% of the tensor pipe taken: no unit is full,
+// the latencies of its 28 warps bind.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1466,7 +1467,7 @@ struct Place {
 template <int NB, int N>
 bool plan(const TreeParams& p, Plan& pl) {
   // in order of preference: stages of V^ and P, slots of a code ring
-  static const int tries[6][3] = {{2, 2, 3}, {2, 2, 2}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}};
+  static const int tries[7][3] = {{2, 2, 3}, {2, 2, 2}, {2, 1, 3}, {2, 1, 2}, {1, 1, 3}, {1, 1, 2}, {1, 1, 1}};
   for (const auto& t : tries) {
     pl = Plan{};
     Place at;

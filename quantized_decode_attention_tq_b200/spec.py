@@ -10,18 +10,21 @@ import struct
 
 import numpy as np
 
-from ._lib import TQ_BF16, TQ_F16, TQ_F32, TQ_MAX_TREE_NODES, CacheBufs, Codebook, KVDesc, Rope, check, lib
+from ._lib import TQ_BF16, TQ_F16, TQ_F32, TQ_MAX_TREE_NODES, Codebook, KVDesc, Rope, check, lib
 from .api import Cache, VOutliers
 
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _ROWS = struct.Struct("PPPi4xqqq")  # tq_rows
-_torch = None
+_BUFS = struct.Struct("PPPPPi4x")   # tq_cache_bufs
+_torch = _int32 = None
 _codes = {}
+_fns = {}
 
 
 def _setup():
-    global _torch
+    global _torch, _int32
     import torch
+    _int32 = torch.int32
     _codes.update({torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16})
     _torch = torch
     return torch
@@ -57,9 +60,11 @@ def _ptr(t, name, dev, contiguous=True):
 def _i32(t, name, dev, shape):
     if t is None:
         return None
-    if t.dtype is not _torch.int32 or t.shape != shape:
+    if t.dtype is not _int32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 of shape {shape}")
-    return _ptr(t, name, dev)
+    if t.get_device() != dev or not t.is_contiguous():
+        return _ptr(t, name, dev)
+    return t.data_ptr()
 
 
 def _status(t, dev):
@@ -72,7 +77,9 @@ def _status(t, dev):
 
 def _call(fn, dev, stream, *args):
     """Run fn(*args, stream) with the tensors' device current."""
-    f, cuda = getattr(lib(), fn), _torch.cuda
+    f, cuda = _fns.get(fn), _torch.cuda
+    if f is None:
+        f = _fns[fn] = getattr(lib(), fn)
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"stream must be on cuda:{dev}, like the tensors of the call")
     if cuda.current_device() == dev:
@@ -80,7 +87,8 @@ def _call(fn, dev, stream, *args):
     else:
         with cuda.device(dev):
             st = f(*args, (cuda.current_stream() if stream is None else stream).cuda_stream)
-    check(fn, st)
+    if st:
+        check(fn, st)
 
 
 # ---- position rotation and per-head norms ----------------------------------
@@ -206,10 +214,15 @@ def decode_attention_tree(cache: Cache, k_cb: Codebook, v_cb: Codebook, q, seq_l
 
 # ---- rows of the cache -------------------------------------------------------
 
-def _bufs(cache: Cache, vo: VOutliers | None, dev) -> CacheBufs:
-    return CacheBufs(_ptr(cache.k_codes, "k_codes", dev), _ptr(cache.k_norms, "k_norms", dev),
-                     _ptr(cache.v_codes, "v_codes", dev), _ptr(cache.v_norms, "v_norms", dev),
-                     None if vo is None else _ptr(vo.values, "values", dev), 0 if vo is None else vo.k)
+def _bufs(cache: Cache, vo: VOutliers | None, dev) -> bytes:
+    """The tq_cache_bufs of a cache."""
+    a, b, c, d = cache.k_codes, cache.k_norms, cache.v_codes, cache.v_norms
+    if not (a.get_device() == b.get_device() == c.get_device() == d.get_device() == dev and a.is_contiguous()
+            and b.is_contiguous() and c.is_contiguous() and d.is_contiguous()):
+        for n in ("k_codes", "k_norms", "v_codes", "v_norms"):
+            _ptr(getattr(cache, n), n, dev)
+    values, k = (0, 0) if vo is None else (_ptr(vo.values, "values", dev), vo.k)
+    return _BUFS.pack(a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), values, k)
 
 
 def cache_compact(cache: Cache, keep, n_keep, start=None, new_lens=None, vo: VOutliers | None = None, status=None,
@@ -222,7 +235,7 @@ def cache_compact(cache: Cache, keep, n_keep, start=None, new_lens=None, vo: VOu
     if keep.dim() != 2:
         raise ValueError("keep must be [B, max_keep]")
     m = keep.shape[1]
-    _call("tq_cache_compact", dev, stream, ctypes.byref(cache.desc), ctypes.byref(_bufs(cache, vo, dev)),
+    _call("tq_cache_compact", dev, stream, ctypes.byref(cache.desc), _bufs(cache, vo, dev),
           _i32(keep, "keep", dev, (b, m)), m, _i32(n_keep, "n_keep", dev, (b,)), _i32(start, "start", dev, (b,)),
           _i32(new_lens, "new_lens", dev, (b,)), _status(status, dev))
 
@@ -234,8 +247,8 @@ def cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, n_rows, max_rows: int
     dev = _device(src.k_codes, "k_codes")
     n = src_slot.shape[0]
     shape = (n,)
-    a = ctypes.byref(_bufs(src, src_vo, dev))
-    b = a if dst is src and dst_vo is src_vo else ctypes.byref(_bufs(dst, dst_vo, dev))
+    a = _bufs(src, src_vo, dev)
+    b = a if dst is src and dst_vo is src_vo else _bufs(dst, dst_vo, dev)
     _call("tq_cache_copy", dev, stream, ctypes.byref(src.desc), a, ctypes.byref(dst.desc), b, n,
           _i32(src_slot, "src_slot", dev, shape), _i32(dst_slot, "dst_slot", dev, shape),
           _i32(src_pos, "src_pos", dev, shape), _i32(dst_pos, "dst_pos", dev, shape),

@@ -122,7 +122,7 @@ def _random_tree(rng, n, roots=2):
 
 
 def _tree_case(seed, batch, hq, hk, dim, kb, vb, cap, lens, n_q, counts=None, masks=None, src="float16", dst="float16",
-               scale=None, cache=None, sign_seed=0, q=None):
+               scale=None, cache=None, sign_seed=0, q=None, v_levels=1.0):
     torch = torch_mod()
     rng = np.random.default_rng(seed)
     cache = cache or R.random_cache(rng, batch, hk, cap, dim, kb, vb)
@@ -140,14 +140,18 @@ def _tree_case(seed, batch, hq, hk, dim, kb, vb, cap, lens, n_q, counts=None, ma
     ws.fill_(255)  # NaN everywhere: any content is allowed
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     scale = dim ** -0.5 if scale is None else scale
-    tq.decode_attention_tree(dc, tq.make_codebook(kb), tq.make_codebook(vb), qd, to_dev(lens), to_dev(masks), scale, out,
-                             ws, n_nodes=None if counts is None else to_dev(cnt.astype(np.int32)), status=status)
+    v_cb = tq.make_codebook(vb)
+    for i in range(1 << vb):  # the sum over V is linear in its levels
+        v_cb.centroids[i] *= v_levels
+    tq.decode_attention_tree(dc, tq.make_codebook(kb), v_cb, qd, to_dev(lens), to_dev(masks), scale, out, ws,
+                             n_nodes=None if counts is None else to_dev(cnt.astype(np.int32)), status=status)
     torch.cuda.synchronize()
     assert tq.read_device_status(status) == 0
     ref, spread, score = R.tree_attention(_np(qd), cache, kb, vb, lens, cnt, masks, scale, sign_seed)
     got = _np(out)
     past = np.isnan(ref)
     assert np.all(got[past] == 3.0)
+    got = got / v_levels
     R.check_tree(got, ref, spread, score, torch.finfo(_dt(dst)).eps)
     return got, ref
 
@@ -156,6 +160,13 @@ def _tree_case(seed, batch, hq, hk, dim, kb, vb, cap, lens, n_q, counts=None, ma
 def test_tree_bits(kb, vb):
     _tree_case(kb * 4 + vb, 2, 8, 2, 128, kb, vb, 300, [300, 131], 7)
     _tree_case(kb * 4 + vb, 1, 4, 2, 256, kb, vb, 200, [197], 5, src="bfloat16", dst="bfloat16")
+
+
+@pytest.mark.parametrize("dim,bits", [(128, 4), (128, 3), (256, 4), (256, 3), (256, 2)])
+@pytest.mark.parametrize("v_levels", [1.0, 1.25])
+def test_tree_wide_groups_with_equal_and_unequal_codebooks(dim, bits, v_levels):
+    # 130 rows: the widest row groups and the fullest shared memory; K and V share a table or not
+    _tree_case(dim + bits, 1, 10, 1, dim, bits, bits, 400, [390], 13, v_levels=v_levels)
 
 
 @pytest.mark.parametrize("hq,hk,n_q", [(1, 1, 1), (1, 1, 2), (4, 4, 3), (8, 2, 4), (8, 1, 5), (12, 4, 16), (32, 8, 8),
