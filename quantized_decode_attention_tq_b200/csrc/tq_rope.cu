@@ -129,7 +129,7 @@ enum Layout { kHalves = 0, kNeighbours = 1, kAnyHalves = 2 };  // kAnyHalves: ro
 template <int IN, int OUT, int LPR, int MODE>
 __global__ void __launch_bounds__(kRopeThreads, IN == TQ_F32 || MODE == kAnyHalves ? 3 : 4)
 rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastDiv by_seq) {
-  constexpr bool GEN = MODE == kAnyHalves, INTER = MODE == kNeighbours, split = MODE == kHalves;
+  constexpr bool GEN = MODE == kAnyHalves, split = MODE == kHalves;
   constexpr int kGroups = kRopeThreads / LPR;
   constexpr int VI = Elem<IN>::kVec, VO = Elem<OUT>::kVec, kIn = IN == TQ_F32 ? 4 : 2, kOut = OUT == TQ_F32 ? 4 : 2;
   struct Base {
@@ -158,11 +158,13 @@ rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastD
 
   // chunk indices of this lane (see the file comment)
   const int hc = hp / 8;
-  const int ca = split ? (sub < hc ? sub : 2 * hc + 2 * (sub - hc)) : 2 * sub;
-  const int cb = split && sub < hc ? sub + hc : ca + 1;
+  // (neighbours: chunks sub and sub + D / 16, so that lanes read side by side)
+  const int ca = split ? (sub < hc ? sub : 2 * hc + 2 * (sub - hc)) : GEN ? 2 * sub : sub;
+  const int cb = split ? (sub < hc ? sub + hc : ca + 1) : GEN ? ca + 1 : sub + D / 16;
   const bool has = 16 * sub < D;  // rows of 384 leave the last lanes idle
-  const int m0 = 8 * sub;         // this lane's pairs m0 .. m0 + 7
-  const bool all = !GEN && m0 + 8 <= hp, some = !GEN && m0 < hp;  // all or some of them turn
+  // this lane's pairs: ma .. ma + 3 and mb .. mb + 3; whether all or some of them turn
+  const int ma = split ? 8 * sub : 4 * ca, mb = split ? ma + 4 : 4 * cb;
+  const bool all = !GEN && has && mb + 4 <= hp, some = !GEN && has && ma < hp;
 
   // where each token's rows of each side begin
   if (tid < 3 * toks) {
@@ -226,24 +228,16 @@ rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastD
     char* const out = cur.out;
     const float* ct = cos_t + cur.token * pitch;
     const float* st = sin_t + cur.token * pitch;
-    float u[8], v[8];  // halves: the two halves; neighbours: even and odd elements
-    {
-      float xa[8], xb[8];
-      unpack8<IN>(cur.a, xa);
-      unpack8<IN>(cur.b, xb);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        u[k] = INTER ? (k < 4 ? xa[(2 * k) & 7] : xb[(2 * k) & 7]) : xa[k];
-        v[k] = INTER ? (k < 4 ? xa[(2 * k + 1) & 7] : xb[(2 * k + 1) & 7]) : xb[k];
-      }
-    }
+    float xa[8], xb[8];  // the lane's two chunks
+    unpack8<IN>(cur.a, xa);
+    unpack8<IN>(cur.b, xb);
     load(item + kGroups);
     if (p.norm) {  // every lane takes part in the shuffles
       float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < 8; k += 2) {
-        q = fma2(make_float2(u[k], u[k + 1]), make_float2(u[k], u[k + 1]), q);
-        q = fma2(make_float2(v[k], v[k + 1]), make_float2(v[k], v[k + 1]), q);
+        q = fma2(make_float2(xa[k], xa[k + 1]), make_float2(xa[k], xa[k + 1]), q);
+        q = fma2(make_float2(xb[k], xb[k + 1]), make_float2(xb[k], xb[k + 1]), q);
       }
       float ss = out ? q.x + q.y : 0.0f;
 #pragma unroll
@@ -254,56 +248,53 @@ rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastD
         const float4* wa = reinterpret_cast<const float4*>(wts + s * D + 8 * ca);
         const float4* wb = reinterpret_cast<const float4*>(wts + s * D + 8 * cb);
         const float4 a0 = wa[0], a1 = wa[1], b0 = wb[0], b1 = wb[1];
-        const float ea[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        const float eb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        const float2 ea[4] = {{a0.x, a0.y}, {a0.z, a0.w}, {a1.x, a1.y}, {a1.z, a1.w}};
+        const float2 eb[4] = {{b0.x, b0.y}, {b0.z, b0.w}, {b1.x, b1.y}, {b1.z, b1.w}};
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
-          float wu[2], wv[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int e = k + j;
-            wu[j] = INTER ? (e < 4 ? ea[(2 * e) & 7] : eb[(2 * e) & 7]) : ea[e];
-            wv[j] = INTER ? (e < 4 ? ea[(2 * e + 1) & 7] : eb[(2 * e + 1) & 7]) : eb[e];
-          }
-          const float2 x = mul2(make_float2(u[k], u[k + 1]), mul2(make_float2(wu[0], wu[1]), i2));
-          const float2 y = mul2(make_float2(v[k], v[k + 1]), mul2(make_float2(wv[0], wv[1]), i2));
-          u[k] = x.x, u[k + 1] = x.y;
-          v[k] = y.x, v[k + 1] = y.y;
+          const float2 x = mul2(make_float2(xa[k], xa[k + 1]), mul2(ea[k / 2], i2));
+          const float2 y = mul2(make_float2(xb[k], xb[k + 1]), mul2(eb[k / 2], i2));
+          xa[k] = x.x, xa[k + 1] = x.y;
+          xb[k] = y.x, xb[k + 1] = y.y;
         }
       }
     }
-    if (s < 2) {
-      if (all) {
-        const float4* c4 = reinterpret_cast<const float4*>(ct + m0);
-        const float4* n4 = reinterpret_cast<const float4*>(st + m0);
-        const float4 c0 = c4[0], c1 = c4[1], n0 = n4[0], n1 = n4[1];
+    if (s < 2 && some) {
+      const float4 c0 = *reinterpret_cast<const float4*>(ct + ma), c1 = *reinterpret_cast<const float4*>(ct + mb);
+      const float4 n0 = *reinterpret_cast<const float4*>(st + ma), n1 = *reinterpret_cast<const float4*>(st + mb);
+      if constexpr (split) {  // pairs (xa[k], xb[k]), two at a time
         const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
         const float2 sn[4] = {{n0.x, n0.y}, {n0.z, n0.w}, {n1.x, n1.y}, {n1.z, n1.w}};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 c = cs[k], n = sn[k];
-          const float2 x = make_float2(u[2 * k], u[2 * k + 1]), y = make_float2(v[2 * k], v[2 * k + 1]);
+          const float2 x = make_float2(xa[2 * k], xa[2 * k + 1]), y = make_float2(xb[2 * k], xb[2 * k + 1]);
           const float2 z = mul2(y, n), o = fma2(x, c, make_float2(-z.x, -z.y)), q = fma2(y, c, mul2(x, n));
-          u[2 * k] = o.x, u[2 * k + 1] = o.y;
-          v[2 * k] = q.x, v[2 * k + 1] = q.y;
+          xa[2 * k] = o.x, xa[2 * k + 1] = o.y;
+          xb[2 * k] = q.x, xb[2 * k + 1] = q.y;
         }
-      } else if (some) {
+      } else {  // pairs of neighbours, perhaps not all turning
+        const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float sn[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (m0 + k < hp) {
-            const float c = ct[m0 + k], n = st[m0 + k], x = u[k];
-            u[k] = x * c - v[k] * n;
-            v[k] = v[k] * c + x * n;
+        for (int k = 0; k < 8; ++k) {
+          float& x = k < 4 ? xa[(2 * k) & 7] : xb[(2 * k) & 7];
+          float& y = k < 4 ? xa[(2 * k + 1) & 7] : xb[(2 * k + 1) & 7];
+          if (all || (k < 4 ? ma + k : mb + k - 4) < hp) {
+            const float o = x * cs[k] - y * sn[k];
+            y = y * cs[k] + x * sn[k];
+            x = o;
           }
+        }
       }
     }
-    if constexpr (GEN) {  // u, v: the lane's 16 consecutive elements
+    if constexpr (GEN) {  // xa, xb: the lane's 16 consecutive elements
       float* copy = scratch + group * (D + D / 16);
       if (has) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          copy[17 * sub + k] = u[k];
-          copy[17 * sub + 8 + k] = v[k];
+          copy[17 * sub + k] = xa[k];
+          copy[17 * sub + 8 + k] = xb[k];
         }
       }
       __syncwarp();
@@ -311,7 +302,7 @@ rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastD
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int e = 16 * sub + k;
-          float& x = k < 8 ? u[k & 7] : v[k & 7];
+          float& x = k < 8 ? xa[k & 7] : xb[k & 7];
           if (e < 2 * hp) {
             const int m = e < hp ? e : e - hp;
             const float n = st[padded(m)];
@@ -324,14 +315,8 @@ rope_kernel(const __grid_constant__ RopeParams p, int TT, FastDiv by_rows, FastD
     if (out) {
       uint4* dst = reinterpret_cast<uint4*>(out);
       uint4 oa[VO], ob[VO];
-      float ya[8], yb[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ya[k] = INTER ? (k & 1 ? v[k / 2] : u[k / 2]) : u[k];
-        yb[k] = INTER ? (k & 1 ? v[4 + k / 2] : u[4 + k / 2]) : v[k];
-      }
-      pack8<OUT>(ya, oa);
-      pack8<OUT>(yb, ob);
+      pack8<OUT>(xa, oa);
+      pack8<OUT>(xb, ob);
 #pragma unroll
       for (int k = 0; k < VO; ++k) {
         dst[ca * VO + k] = oa[k];
