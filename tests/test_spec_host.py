@@ -182,3 +182,8 @@ def test_binding_refuses_before_the_library():
         tq.qk_norm_rope(None, q=x, q_out=x)  # not on a GPU
     with pytest.raises(ValueError):
         tq.qk_norm_rope(None)
+
+
+def test_binding_refuses_max_rows_that_its_int_cannot_hold():
+    with pytest.raises(ValueError, match="max_rows"):
+        tq.cache_copy(None, None, None, None, None, 2 ** 32)
