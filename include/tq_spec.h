@@ -137,6 +137,10 @@ size_t tq_tree_workspace_size(const tq_kv_desc* desc, int q_heads, int n_q);
  *   - workspace: tq_tree_workspace_size() bytes, 256-byte aligned, any
  *     content; calls that share one must not overlap in time.  Three launches
  *     (queries, attention, join), the last two as programmatic dependents.
+ *   - Every wait inside the kernel is bounded, at 2^20 tries of about a
+ *     microsecond (fewer if the environment sets TQ_TREE_WAIT_TRIES before the
+ *     process's first call).  One that runs out sets TQ_DEV_INTERNAL: out is
+ *     invalid, nothing of the call is left in flight, the context stays usable.
  * seq_lens, limits and errors otherwise as tq_decode_attention (head_dim 128
  * or 256, even seq_cap, batch <= 2048, any q_heads / kv_heads ratio).
  */

@@ -76,6 +76,7 @@ struct TreeParams {
   int k_bits, v_bits;
   int batch, kv_heads, q_heads, head_dim, seq_cap, n_q;
   float score_mult;  // scale * log2(e) / 128
+  int wait_tries;    // limit of a wait inside the kernel, set by launch_tree
   void* workspace;
 };
 size_t tree_workspace_bytes(int batch, int kv_heads, int q_heads, int head_dim, int n_q);

@@ -36,7 +36,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <type_traits>
 
@@ -176,17 +178,30 @@ __device__ __forceinline__ bool bar_try(uint32_t a, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Wait for a phase, for at most about a second (2^20 tries of a microsecond):
-// then the abort word is set, every later wait returns at once, the loops run
-// to their end on whatever the buffers hold (all accesses stay in bounds), and
-// the status word says so.
-__device__ __forceinline__ void bar_wait(uint32_t a, uint32_t parity, uint32_t abort_word, uint32_t* status) {
+// Wait for a phase, for at most as many tries of about a microsecond as the
+// limit word says.  One that runs out sets the word to zero (aborted) and
+// reports it.  From then on every wait returns at once, no copy is issued, the
+// loops run to their end on whatever the buffers hold (all accesses stay in
+// bounds), and what is in flight is drained (bar_drain).
+__device__ __forceinline__ void bar_wait(uint32_t a, uint32_t parity, uint32_t limit_word, uint32_t* status) {
 #pragma unroll 1
-  for (int i = 0; i < (1 << 20); ++i) {
-    if (bar_try(a, parity)) return;
-    if (lds32(abort_word)) return;
+  for (uint32_t i = 1; !bar_try(a, parity); ++i) {
+    const uint32_t limit = lds32(limit_word);
+    if (i < limit) continue;
+    if (limit != 0) {
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(limit_word), "r"(0) : "memory");
+      if (status) atomicOr(status, TQ_DEV_INTERNAL);
+    }
+    return;
   }
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(abort_word), "r"(1) : "memory");
+}
+// Wait for a copy or a product that was issued, whether or not the kernel was
+// aborted: neither shared nor tensor memory may go while one is in flight.
+// Both end by themselves; the limit is a second here too.
+__device__ __forceinline__ void bar_drain(uint32_t a, uint32_t parity, uint32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i)
+    if (bar_try(a, parity)) return;
   if (status) atomicOr(status, TQ_DEV_INTERNAL);
 }
 
@@ -571,12 +586,12 @@ __device__ __forceinline__ long long out_row(const Params& P, int b, int kvh, in
 
 // barriers, two stages each but the last
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty = 10, kPFull = 12, kPFree = 14, kQFull = 16,
-           kQFree = 17, kRingFull = 18, kRingFree = 24, kBars = 30 };  // rings: three slots for K, three for V
+           kQFree = 17, kRingFull = 18, kRingFree = 24, kDrain = 30, kBars = 32 };  // rings: three slots for K, three for V
 
 // word offsets in the misc area
 template <int NB, int N>
 struct Misc {
-  static constexpr int kAbort = 0, kTmem = 1, kAnyEmpty = 2, kVmax = 4;      // [16]
+  static constexpr int kLimit = 0, kTmem = 1, kAnyEmpty = 2, kRing = 3, kUnits = 4, kVmax = 8;  // [16]
   static constexpr int kMoff = kVmax + 16;                                   // [N]
   static constexpr int kAlpha = kMoff + N;                                   // [N]
   static constexpr int kRed = kAlpha + N;                                    // [4][N]
@@ -621,9 +636,10 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   uint32_t* misc = reinterpret_cast<uint32_t*>(gen(pl.misc));
   float* miscf = reinterpret_cast<float*>(misc);
   int* prefix = reinterpret_cast<int*>(gen(pl.prefix));
-  const uint32_t abort_word = pl.misc + 4 * M::kAbort;
+  const uint32_t limit_word = pl.misc + 4 * M::kLimit;
   auto bar = [&](int i) { return pl.bar + 8u * (uint32_t)i; };
-  auto wait = [&](int i, uint32_t parity) { bar_wait(bar(i), parity, abort_word, p.status); };
+  auto wait = [&](int i, uint32_t parity) { bar_wait(bar(i), parity, limit_word, p.status); };
+  auto aborted = [&]() { return lds32(limit_word) == 0; };
 
   // ---- set-up: barriers, tensor memory, code tables, lengths ----------------
   if (tid == 0) {
@@ -636,6 +652,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       bar_init(bar(kSEmpty + s), kSoftWarps);
       bar_init(bar(kPFull + s), kSoftWarps);
       bar_init(bar(kPFree + s), 1);
+      bar_init(bar(kDrain + s), 1);
     }
     bar_init(bar(kQFull), 1);
     bar_init(bar(kQFree), 1);
@@ -643,7 +660,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       bar_init(bar(kRingFull + r), 1);
       bar_init(bar(kRingFree + r), 4);
     }
-    misc[M::kAbort] = 0;
+    misc[M::kLimit] = (uint32_t)p.wait_tries;
     misc[M::kAnyEmpty] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1158,8 +1175,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
         }
         x = sg.begin + sg.hi;
       }
-      // nothing is in flight when tensor memory is freed (every S product was
-      // waited for by the softmax warps)
+      // no product is in flight when tensor memory is freed (the softmax warps
+      // waited for every score product)
       if (tile_no > 0) wait(kPFree + p_stage(tile_no - 1), p_phase(tile_no - 1));
     } else if (warp == Ro::kMmaWarp + 2 && lane == 0) {
       // Codes into the rings: a tile's positions are contiguous in the cache.
@@ -1167,7 +1184,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       // and their weights are zero.
       const uint32_t depth = (uint32_t)pl.depth;
       uint32_t slot = 0, free_ph = 1;
-      for (long long x = begin; x < end;) {
+      bool stop = false, half = false;  // half: K's copy of this slot was issued, V's not
+      for (long long x = begin; x < end && !stop;) {
         const Seg sg = find(cut, x, end, P.n_hg);
         const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
         const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
@@ -1177,11 +1195,22 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
           for (int side = 0; side < 2; ++side) {
             const uint32_t row_bytes = NB * 16u * (uint32_t)(side ? p.v_bits : p.k_bits);
             const uint8_t* src = (side ? p.v_codes : p.k_codes) + (row0 + (size_t)tile * kTok) * row_bytes;
-            wait(kRingFree + 3 * side + (int)slot, free_ph);
+            // Aborted, the slot's last copy may still be in flight: a second
+            // one would arrive on a barrier that expects no arrival.  Heads of
+            // one block look once for both sides (132 and 137 us against 134 and
+            // 138 at 16 and 32 columns); in heads of two K would wait for V
+            // (258 against 251 us).
+            if (NB == 2 || side == 0) {
+              if (NB == 1) wait(kRingFree + 3 + (int)slot, free_ph);
+              wait(kRingFree + 3 * side + (int)slot, free_ph);
+              if ((stop = aborted())) break;
+            }
             fence_async_smem();  // the slot's reads before the copy
             bulk_copy((side ? pl.ring_v : pl.ring_k) + slot * (kTok * row_bytes), src, rows * row_bytes,
                       bar(kRingFull + 3 * side + (int)slot));
+            half = side == 0;
           }
+          if (stop) break;
           if (++slot == depth) {
             slot = 0;
             free_ph ^= 1;
@@ -1189,7 +1218,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
         }
         x = sg.begin + sg.hi;
       }
-      if (lds32(abort_word)) __nanosleep(1000000);  // copies may be in flight: they end by themselves
+      misc[M::kRing] = 4 * slot + 2 * free_ph + (half ? 1 : 0);
     } else if (warp == Ro::kMmaWarp + 3 && lane == 0) {
       // Q^ of each unit, as the query kernel left it; and the join's record
       Join j{};
@@ -1205,16 +1234,37 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       for (long long x = begin; x < end; ++seg_no) {
         const Seg sg = find(cut, x, end, P.n_hg);
         wait(kQFree, (seg_no & 1) ^ 1);
+        if (aborted()) break;  // as for the codes
         bulk_copy(pl.q, P.ws_q + ((size_t)sg.b * ub + sg.r) * (4 * NB * kQPanel), 4 * NB * kQPanel, bar(kQFull));
         x = sg.begin + sg.hi;
       }
-      if (lds32(abort_word)) __nanosleep(1000000);
+      misc[M::kUnits] = seg_no;
     }
   }
 
   tc_before();
   __syncthreads();
   tc_after();
+  if (misc[M::kLimit] == 0) {  // waits were cut short: wait for what is in flight
+    if (warp == Ro::kMmaWarp || warp == Ro::kMmaWarp + 1) {  // the products that this warp issued
+      const uint32_t b = bar(kDrain + warp - Ro::kMmaWarp);
+      if (elect_one()) tc_commit(b);
+      __syncwarp();
+      bar_drain(b, 0, p.status);
+    } else if (warp == Ro::kMmaWarp + 2) {
+      // Slots below the next one were last filled in this pass over the ring,
+      // the others in the pass before (at first none was, and parity 1 is over).
+      const uint32_t slot = misc[M::kRing] >> 2, before = (misc[M::kRing] >> 1) & 1u, half = misc[M::kRing] & 1u;
+#pragma unroll 1
+      for (uint32_t i = 0; i < 2 * (uint32_t)pl.depth; ++i) {
+        const uint32_t k = i & 1u, n = i >> 1;
+        bar_drain(bar(kRingFull + 3 * (int)k + (int)n), n < slot + (k == 0 ? half : 0u) ? before ^ 1u : before, p.status);
+      }
+    } else if (warp == Ro::kMmaWarp + 3 && misc[M::kUnits] > 0) {
+      bar_drain(bar(kQFull), (misc[M::kUnits] - 1) & 1u, p.status);
+    }
+    __syncthreads();
+  }
   if (warp == Ro::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
   // ---- rows of empty sequences are zero
@@ -1589,8 +1639,15 @@ size_t tree_workspace_bytes(int batch, int kv_heads, int q_heads, int head_dim, 
 }
 
 int launch_tree(const TreeParams& t, cudaStream_t stream) {
+  // tries of a wait (see bar_wait), read once a process
+  static const int tries = [] {
+    const char* s = std::getenv("TQ_TREE_WAIT_TRIES");
+    const long n = s ? std::strtol(s, nullptr, 10) : 1L << 20;
+    return (int)std::min(std::max(n, 1L), 1L << 20);
+  }();
   tree::Params P{};
   P.t = t;
+  P.t.wait_tries = tries;
   P.kscale = tree::centroid_scale(t.kcent, t.k_bits);
   P.vscale = tree::centroid_scale(t.vcent, t.v_bits);
   P.klev = tree::level_bytes(t.kcent, P.kscale, t.k_bits);

@@ -1,0 +1,57 @@
+"""The tree kernel's pipeline over many tiles: several tiles in every CTA (stage
+and phase reuse, rescaling, cuts inside units), and waits that run out."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+import quantized_decode_attention_tq_b200 as tq
+
+from . import _spec_ref as R
+from ._parity import to_dev, torch_mod
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+RUN_OUT = """
+import numpy as np, torch
+import quantized_decode_attention_tq_b200 as tq
+from quantized_decode_attention_tq_b200._lib import TQ_DEV_INTERNAL
+from tests import _spec_ref as R
+dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+rng, n, states = np.random.default_rng(0), 6, set()
+for hq, hk, dim in ((8, 4, 128), (32, 2, 256), (64, 4, 128)):
+    kc, kn, vc, vn = R.random_cache(rng, 4, hk, 6000, dim, 3, 3)
+    desc = tq.kv_desc(4, hk, dim, 6000, 3, 3)
+    cache = tq.Cache(desc, dev(kc), dev(kn.view(np.int16)), dev(vc), dev(vn.view(np.int16)))
+    cb = tq.make_codebook(3)
+    q = torch.randn(4, n, hq, dim, device="cuda", dtype=torch.float16)
+    masks = dev(np.stack([tq.tree_masks([-1, 0, 0, 1, 2, 4])[0]] * 4))
+    lens = dev(np.array([6000, 5999, 130, 4000], dtype=np.int32))
+    out, ws = torch.zeros_like(q), tq.alloc_tree_workspace(desc, hq, n)
+    for _ in range(10):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        tq.decode_attention_tree(cache, cb, cb, q, lens, masks, dim ** -0.5, out, ws, status=status)
+        states.add(tq.read_device_status(status))
+    # the context is usable: a chain of nodes by the other kernel, against the reference's first row
+    multi = torch.zeros(q.shape, device="cuda")
+    tq.decode_attention_multi(cache, cb, cb, q, lens, dim ** -0.5, multi, tq.alloc_workspace(desc, hq * n))
+    chain = np.stack([tq.tree_masks([-1, 0, 1, 2, 3, 4])[0]] * 4)
+    ref, spread, score = R.tree_attention(q[:, :1].double().cpu().numpy(), (kc, kn, vc, vn), 3, 3,
+                                          (lens - n + 1).tolist(), [1] * 4, chain[:, :1], dim ** -0.5)
+    R.check_tree(multi[:, :1].double().cpu().numpy(), ref, spread, score, 2.0 ** -23)
+assert states <= {0, TQ_DEV_INTERNAL}, states
+print("states", sorted(states))
+"""
+
+
+def test_waits_that_run_out_are_reported_and_leave_the_context_usable():
+    """The first wait for a score product takes longer than one try: the kernel
+    reports it, drains what it issued and returns."""
+    for tries, want in (("1", "states [8]"), ("1000000", "states [0]")):
+        r = subprocess.run([sys.executable, "-c", RUN_OUT], cwd=ROOT, env={**os.environ, "TQ_TREE_WAIT_TRIES": tries},
+                           capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and want in r.stdout, (tries, r.stdout, r.stderr[-2000:])
