@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "tq_spec_internal.h"
+#include "tq_tree_cut.h"
 
 namespace tq {
 namespace tree {
@@ -381,78 +382,6 @@ __device__ __forceinline__ void wht(float (&v)[NB][4], int lane) {
   }
 }
 
-// ------------------------------------------------------------------ split --
-
-// a / b for 0 <= a, 0 < b: 32-bit where both fit (a 64-bit division is a long
-// subroutine, and several stand in a launch's critical path)
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
-  return a / b;
-}
-
-// The flattened tiles [0, total) are cut into `parts` ranges of equal cost: a
-// tile costs 1, and the end of a unit kSwitch more (the partial, the next
-// unit's query and the references of its first tile).  A tree of 64 nodes on
-// 131072 positions: 277 us with no such cost, 272 with 3, 5 or 8; other cases
-// within 1%.  With few tiles per part the boundary counts nothing, so that no
-// range is empty.
-constexpr int kSwitch = 3;
-struct Cut {
-  const int* prefix;  // tiles before each batch entry
-  int batch, ub;      // ub: units per batch entry
-  long long total, parts, sw, cost;
-  __device__ Cut(const int* pre, int b, int units, int grid) : prefix(pre), batch(b), ub(units) {
-    total = (long long)pre[b] * units;
-    parts = min((long long)grid, total);
-    sw = total >= 4LL * kSwitch * grid ? kSwitch : 0;
-    cost = total + sw * units * (long long)b;
-  }
-  __device__ long long before(int b) const { return (long long)ub * (prefix[b] + sw * b); }  // cost of the entries before b
-  // first tile of part c
-  __device__ long long start(long long c) const {
-    if (c >= parts) return total;
-    const long long y = quotient(c * cost, parts);
-    if (sw == 0) return y;
-    int lo = 0, hi = batch;  // the last entry whose cost starts at or before y
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before(mid) <= y) lo = mid;
-      else hi = mid;
-    }
-    const long long nt = prefix[lo + 1] - prefix[lo], rest = y - before(lo), r = quotient(rest, nt + sw);
-    return (long long)ub * prefix[lo] + r * nt + min(rest - r * (nt + sw), nt);
-  }
-  // the part that holds tile t of unit r of batch entry b
-  __device__ long long part_of(int b, int r, int t) const {
-    const long long nt = prefix[b + 1] - prefix[b];
-    return quotient((before(b) + r * (nt + sw) + t + 1) * parts - 1, cost);
-  }
-};
-
-struct Seg {
-  int b, r, kvh, hg, nt, lo, hi;
-  long long begin;  // first tile of the unit
-};
-__device__ __forceinline__ Seg find(const Cut& cut, long long x, long long end, int n_hg) {
-  int lo = 0, hi = cut.batch;  // the last entry whose tiles start at or before x
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)cut.prefix[mid] * cut.ub <= x) lo = mid;
-    else hi = mid;
-  }
-  Seg s;
-  s.b = lo;
-  s.nt = cut.prefix[lo + 1] - cut.prefix[lo];
-  const long long first = (long long)cut.prefix[lo] * cut.ub;
-  s.r = (int)quotient(x - first, s.nt);
-  s.kvh = s.r / n_hg;
-  s.hg = s.r % n_hg;
-  s.begin = first + (long long)s.r * s.nt;
-  s.lo = (int)(x - s.begin);
-  s.hi = (int)min(end - s.begin, (long long)s.nt);
-  return s;
-}
-
 // ------------------------------------------------------------ codes -> fp16 --
 
 // Address of pair q (codes 2q, 2q + 1) of a B-bit stream in the lane's table:
@@ -591,13 +520,13 @@ enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty
 // word offsets in the misc area
 template <int NB, int N>
 struct Misc {
-  static constexpr int kLimit = 0, kTmem = 1, kAnyEmpty = 2, kRing = 3, kUnits = 4, kVmax = 8;  // [16]
+  static constexpr int kLimit = 0, kTmem = 1, kAnyEmpty = 2, kRing = 3, kUnits = 4, kBegin = 6, kVmax = 8;  // [16]
   static constexpr int kMoff = kVmax + 16;                                   // [N]
   static constexpr int kAlpha = kMoff + N;                                   // [N]
   static constexpr int kRed = kAlpha + N;                                    // [4][N]
   static constexpr int kMask = kRed + 4 * N;                                 // [N] 64-bit
-  static constexpr int kScan = kMask + 2 * N;                                // [16]
-  static constexpr int kNorm = kScan + 16;                                   // [4 tiles][block][K, V][128]
+  static constexpr int kScan = kMask + 2 * N;                                // [2][16]
+  static constexpr int kNorm = kScan + 32;                                   // [4 tiles][block][K, V][128]
   static constexpr int kWords = kNorm + 4 * NB * 2 * kTok;
 };
 
@@ -670,7 +599,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  int lens_r[4], local = 0;  // kMaxBatch / 512
+  int lens_r[4], local = 0, local_live = 0;  // kMaxBatch / 512; tiles, entries that have some
   const int per = (p.batch + 511) / 512;
   if (tid < 512) {
 #pragma unroll
@@ -688,17 +617,23 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   fill(p.v_bits, p.vcent, P.vscale, pl.lut_v);
   bool empty = false;
   if (tid < 512) {
+    int live = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i >= per || tid * per + i >= p.batch) break;
+      const bool there = i < per && tid * per + i < p.batch;
       const int len = min(max(lens_r[i], 0), p.seq_cap);
-      if (blockIdx.x == 0 && p.status) {
+      if (there && blockIdx.x == 0 && p.status) {
         const int nn = p.n_nodes ? __ldg(p.n_nodes + tid * per + i) : 0;
         if (len != lens_r[i] || nn < 0 || nn > p.n_q) atomicOr(p.status, TQ_DEV_LEN_RANGE);
       }
       lens_r[i] = (len + kTok - 1) / kTok;
       local += lens_r[i];
-      empty |= len == 0;
+      empty |= there && len == 0;
+      if (i < per) {
+        const uint32_t have = __ballot_sync(0xffffffffu, len > 0);
+        local_live += __popc(have & ((1u << lane) - 1u));
+        live += __popc(have);
+      }
     }
     int incl = local;
 #pragma unroll
@@ -706,29 +641,45 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) misc[M::kScan + warp] = (uint32_t)incl;
+    if (lane == 31) {
+      misc[M::kScan + warp] = (uint32_t)incl;
+      misc[M::kScan + 16 + warp] = (uint32_t)live;
+    }
     local = incl - local;  // before this thread, inside the warp
   }
   tc_before();
   __syncthreads();
   tc_after();
+  const int ub = p.kv_heads * P.n_hg;
+  const uint32_t warp_tiles = lane < 16 ? misc[M::kScan + lane] : 0;
+  const int sw = switch_length((long long)__reduce_add_sync(0xffffffffu, warp_tiles) * ub, (int)gridDim.x);
   if (tid < 512) {
-    int run = local;
-    for (int w = 0; w < warp; ++w) run += (int)misc[M::kScan + w];
+    int run = local + (int)__reduce_add_sync(0xffffffffu, lane < warp ? warp_tiles : 0u) +
+              sw * (local_live + (int)__reduce_add_sync(0xffffffffu, lane < warp ? misc[M::kScan + 16 + lane] : 0u));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i >= per || tid * per + i >= p.batch) break;
       prefix[tid * per + i] = run;
-      run += lens_r[i];
+      run += unit_length(lens_r[i], sw);
       if (tid * per + i == p.batch - 1) prefix[p.batch] = run;
     }
     if (empty) misc[M::kAnyEmpty] = 1;
   }
   __syncthreads();
   const uint32_t tmem = misc[M::kTmem];
-  const int ub = p.kv_heads * P.n_hg;
-  const Cut cut(prefix, p.batch, ub, gridDim.x);
-  const long long begin = cut.start(blockIdx.x), end = blockIdx.x < cut.parts ? cut.start(blockIdx.x + 1) : begin;
+  const Cut cut(prefix, p.batch, ub, sw, (int)gridDim.x);
+  // This CTA's part of the line; its beginning is kept in shared memory, not in
+  // two registers of every role.
+  int span;
+  {
+    const long long begin = cut.start(blockIdx.x);
+    span = blockIdx.x < cut.parts ? (int)(cut.start(blockIdx.x + 1) - begin) : 0;
+    *reinterpret_cast<volatile long long*>(misc + M::kBegin) = begin;  // every thread: the same value
+  }
+  auto segment = [&](int x) {  // the unit at x from the beginning
+    const long long begin = *reinterpret_cast<volatile long long*>(misc + M::kBegin);
+    return cut.find(begin + x, begin + span, P.n_hg);
+  };
   const uint32_t tm_o = tmem + kColsO;
   // P: tile n uses stage n mod p_stages (1 or 2)
   const uint32_t p_shift = (uint32_t)pl.p_stages - 1;
@@ -749,8 +700,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
     const int gid = 2 + grp;       // named barrier of the group
     uint32_t tile_no = 0, seg_no = 0;  // across segments
     const int rows = (int)P.group.d * p.n_q;  // of a kv-head
-    for (long long x = begin; x < end; ++seg_no) {
-      const Seg sg = find(cut, x, end, P.n_hg);
+    for (int x = 0; x < span; ++seg_no) {
+      const Seg sg = segment(x);
       const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
       const int nodes = clamp_nodes(p, sg.b), ctx = len - nodes;
       named_sync(1, 32 * kSoftWarps);  // every group is done with the unit before
@@ -1008,7 +959,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
           emit_row<NB>(p, v, __ldcg(ml + 2 * n + 1), lane, (size_t)row);
         }
       }
-      x = sg.begin + sg.hi;
+      x += sg.nt - sg.lo + sw;
     }
   } else if (warp < Ro::kMmaWarp) {
     // ============================================================ dequantise
@@ -1026,8 +977,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       const uint32_t v_row = pl.vt + (uint32_t)tok * 128u + (uint32_t)((tok & 7) << 4);
       const uint32_t shift = V ? (uint32_t)pl.v_stages - 1 : 1u;
       uint32_t slot = 0, slot_ph = 0, stage = 0, stage_ph = 1, tile_no = 0;
-      for (long long x = begin; x < end;) {
-        const Seg sg = find(cut, x, end, P.n_hg);
+      for (int x = 0; x < span;) {
+        const Seg sg = segment(x);
         const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
         const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
         const int tiles = sg.hi - sg.lo;
@@ -1086,7 +1037,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
             slot_ph ^= 1;
           }
         }
-        x = sg.begin + sg.hi;
+        x += sg.nt - sg.lo + sw;
       }
     };
     auto by_bits = [&](int bits, auto side_tag) {
@@ -1108,8 +1059,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       uint32_t ks = 0, kph = 0, tile_no = 0, seg_no = 0;
       const uint64_t dq = smem_desc(pl.q, 16, 1024);
       const uint32_t tm = uniform(tmem);
-      for (long long x = begin; x < end; ++seg_no) {
-        const Seg sg = find(cut, x, end, P.n_hg);
+      for (int x = 0; x < span; ++seg_no) {
+        const Seg sg = segment(x);
         const int tiles = uniform(sg.hi - sg.lo);
         wait(kQFull, seg_no & 1);
         for (int i = 0; i < tiles; ++i, ++tile_no) {
@@ -1140,15 +1091,15 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
         }
         if (elect_one()) tc_commit(bar(kQFree));
         __syncwarp();
-        x = sg.begin + sg.hi;
+        x += sg.nt - sg.lo + sw;
       }
     } else if (warp == Ro::kMmaWarp + 1) {
       constexpr uint32_t id_o = mma_desc(N, true, true);
       uint32_t vs = 0, vph = 0, tile_no = 0;
       const uint64_t dv = smem_desc(pl.vt, kPanel, 1024), dp = smem_desc(pl.pt, kPanel, 1024);
       const uint32_t to = uniform(tm_o);
-      for (long long x = begin; x < end;) {
-        const Seg sg = find(cut, x, end, P.n_hg);
+      for (int x = 0; x < span;) {
+        const Seg sg = segment(x);
         const int tiles = uniform(sg.hi - sg.lo);
         for (int i = 0; i < tiles; ++i, ++tile_no) {
           wait(kPFull + p_stage(tile_no), p_phase(tile_no));
@@ -1173,7 +1124,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
             }
           }
         }
-        x = sg.begin + sg.hi;
+        x += sg.nt - sg.lo + sw;
       }
       // no product is in flight when tensor memory is freed (the softmax warps
       // waited for every score product)
@@ -1185,8 +1136,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       const uint32_t depth = (uint32_t)pl.depth;
       uint32_t slot = 0, free_ph = 1;
       bool stop = false, half = false;  // half: K's copy of this slot was issued, V's not
-      for (long long x = begin; x < end && !stop;) {
-        const Seg sg = find(cut, x, end, P.n_hg);
+      for (int x = 0; x < span && !stop;) {
+        const Seg sg = segment(x);
         const int len = min(max(__ldg(p.seq_lens + sg.b), 0), p.seq_cap);
         const size_t row0 = ((size_t)sg.b * p.kv_heads + sg.kvh) * p.seq_cap;
         for (int tile = sg.lo; tile < sg.hi; ++tile) {
@@ -1216,14 +1167,14 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
             free_ph ^= 1;
           }
         }
-        x = sg.begin + sg.hi;
+        x += sg.nt - sg.lo + sw;
       }
       misc[M::kRing] = 4 * slot + 2 * free_ph + (half ? 1 : 0);
     } else if (warp == Ro::kMmaWarp + 3 && lane == 0) {
       // Q^ of each unit, as the query kernel left it; and the join's record
       Join j{};
-      if (begin < end) {
-        const Seg sg = find(cut, begin, end, P.n_hg);
+      if (span > 0) {
+        const Seg sg = segment(0);
         if (sg.lo > 0 && cut.part_of(sg.b, sg.r, 0) == (long long)blockIdx.x - 1)
           j = Join{sg.b, sg.kvh, sg.hg, (int)blockIdx.x, (int)cut.part_of(sg.b, sg.r, sg.nt - 1), clamp_nodes(p, sg.b)};
       }
@@ -1231,12 +1182,12 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       asm volatile("griddepcontrol.wait;" ::: "memory");
       asm volatile("fence.proxy.async;" ::: "memory");
       uint32_t seg_no = 0;
-      for (long long x = begin; x < end; ++seg_no) {
-        const Seg sg = find(cut, x, end, P.n_hg);
+      for (int x = 0; x < span; ++seg_no) {
+        const Seg sg = segment(x);
         wait(kQFree, (seg_no & 1) ^ 1);
         if (aborted()) break;  // as for the codes
         bulk_copy(pl.q, P.ws_q + ((size_t)sg.b * ub + sg.r) * (4 * NB * kQPanel), 4 * NB * kQPanel, bar(kQFull));
-        x = sg.begin + sg.hi;
+        x += sg.nt - sg.lo + sw;
       }
       misc[M::kUnits] = seg_no;
     }

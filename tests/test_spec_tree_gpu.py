@@ -16,6 +16,60 @@ pytestmark = pytest.mark.gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
+def _tiles(lens, hq, hk, n_q, dim, columns):
+    """128-position tiles of all units, `columns` rows at a time."""
+    groups = -(-(hq // hk) * n_q // columns)
+    return sum(-(-int(x) // 128) for x in lens) * hk * groups
+
+
+def _sms():
+    return torch_mod().cuda.get_device_properties(0).multi_processor_count
+
+
+def _run(desc, cache, hq, n_q, lens, counts, masks, q, dst="float16", v_levels=1.0):
+    """decode_attention_tree over numpy inputs, as fp64; rows that are left alone hold 3."""
+    torch = torch_mod()
+    kc, kn, vc, vn = cache
+    dc = tq.Cache(desc, to_dev(kc), to_dev(kn.view(np.int16)), to_dev(vc), to_dev(vn.view(np.int16)))
+    v_cb = tq.make_codebook(desc.v_bits)
+    for i in range(1 << desc.v_bits):
+        v_cb.centroids[i] *= v_levels
+    qd = torch.from_numpy(q).to(torch.float16).cuda()
+    out = torch.full(q.shape, 3.0, dtype=getattr(torch, dst), device="cuda")
+    ws = tq.alloc_tree_workspace(desc, hq, n_q)
+    ws.fill_(255)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tq.decode_attention_tree(dc, tq.make_codebook(desc.k_bits), v_cb, qd, to_dev(np.asarray(lens, dtype=np.int32)),
+                             to_dev(masks), desc.head_dim ** -0.5, out, ws,
+                             n_nodes=to_dev(np.asarray(counts, dtype=np.int32)), status=status)
+    assert tq.read_device_status(status) == 0
+    return out.double().cpu().numpy() / v_levels, qd.double().cpu().numpy()
+
+
+def _trees(rng, batch, n):
+    return np.stack([tq.tree_masks([-1] + [int(rng.integers(-1, j)) for j in range(1, n)])[0] for _ in range(batch)])
+
+
+def test_mostly_empty_batches():
+    """Two live sequences among 24 slots, with enough tiles for cuts that weigh the units' ends."""
+    rng = np.random.default_rng(1)
+    B, hk, hq, cap, n, live = 24, 16, 32, 7500, 3, {5: 7499, 17: 7400}
+    small = R.random_cache(rng, 2, hk, cap, 128, 3, 3)
+    cache = [np.zeros((B,) + x.shape[1:], x.dtype) for x in small]
+    for x, y in zip(cache, small):
+        x[list(live)] = y
+    lens, counts = [live.get(b, 0) for b in range(B)], [n if b in live or b == 9 else 0 for b in range(B)]
+    assert _tiles(lens, hq, hk, n, 128, 16) > 12 * _sms()
+    masks, q = _trees(rng, B, n), rng.standard_normal((B, n, hq, 128))
+    got, q = _run(tq.kv_desc(B, hk, 128, cap, 3, 3), cache, hq, n, lens, counts, masks, q)
+    at = list(live)
+    ref, spread, score = R.tree_attention(q[at], small, 3, 3, [lens[b] for b in at], [n] * 2, masks[at], 128 ** -0.5)
+    R.check_tree(got[at], ref, spread, score, 2.0 ** -10)
+    for b in range(B):
+        if b not in live:
+            assert np.all(got[b] == (0.0 if b == 9 else 3.0))  # slot 9 drafts over nothing: its rows see nothing
+
+
 RUN_OUT = """
 import numpy as np, torch
 import quantized_decode_attention_tq_b200 as tq
