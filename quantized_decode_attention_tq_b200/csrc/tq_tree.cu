@@ -520,7 +520,7 @@ enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSEmpty
 // word offsets in the misc area
 template <int NB, int N>
 struct Misc {
-  static constexpr int kLimit = 0, kTmem = 1, kAnyEmpty = 2, kRing = 3, kUnits = 4, kBegin = 6, kVmax = 8;  // [16]
+  static constexpr int kLimit = 0, kTmem = 1, kRing = 2, kUnits = 3, kBegin = 4, kVmax = 8;  // [16]
   static constexpr int kMoff = kVmax + 16;                                   // [N]
   static constexpr int kAlpha = kMoff + N;                                   // [N]
   static constexpr int kRed = kAlpha + N;                                    // [4][N]
@@ -590,7 +590,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       bar_init(bar(kRingFree + r), 4);
     }
     misc[M::kLimit] = (uint32_t)p.wait_tries;
-    misc[M::kAnyEmpty] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == Ro::kMmaWarp) {
@@ -615,7 +614,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   };
   if (k_table(NB, p.k_bits) && pl.lut_k != pl.lut_v) fill(p.k_bits, p.kcent, P.kscale, pl.lut_k);
   fill(p.v_bits, p.vcent, P.vscale, pl.lut_v);
-  bool empty = false;
   if (tid < 512) {
     int live = 0;
 #pragma unroll
@@ -628,7 +626,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       }
       lens_r[i] = (len + kTok - 1) / kTok;
       local += lens_r[i];
-      empty |= there && len == 0;
       if (i < per) {
         const uint32_t have = __ballot_sync(0xffffffffu, len > 0);
         local_live += __popc(have & ((1u << lane) - 1u));
@@ -663,7 +660,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       run += unit_length(lens_r[i], sw);
       if (tid * per + i == p.batch - 1) prefix[p.batch] = run;
     }
-    if (empty) misc[M::kAnyEmpty] = 1;
   }
   __syncthreads();
   const uint32_t tmem = misc[M::kTmem];
@@ -1218,21 +1214,13 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
   }
   if (warp == Ro::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
-  // ---- rows of empty sequences are zero
-  if (misc[M::kAnyEmpty]) {
-    const long long rows = (long long)p.batch * p.n_q * p.q_heads;
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-      const long long r = row / p.q_heads;
-      const int b = (int)(r / p.n_q), j = (int)(r % p.n_q);
-      if (prefix[b + 1] != prefix[b] || j >= clamp_nodes(p, b)) continue;
-      for (int d = tid; d < D; d += kThreads) static_cast<uint16_t*>(p.out)[row * D + d] = 0;
-    }
-  }
 }
 
 // The rows of every unit, ready for the score products: q^ = H (s o q) under
 // one power-of-two scale (|q^| <= 128 max |q|, scaled to below 2^15), split into
 // two fp16 terms, in the layout of the kernel's Q^ buffer.  One CTA per unit.
+// The units of an empty sequence have no tiles: their rows see no position, and
+// this kernel writes their zeros.
 template <int NB, int N>
 __global__ void __launch_bounds__(512) query_kernel(const __grid_constant__ Params P) {
   constexpr int D = NB * kBlock, kWarpsQ = 16;
@@ -1244,6 +1232,17 @@ __global__ void __launch_bounds__(512) query_kernel(const __grid_constant__ Para
   const int ub = p.kv_heads * P.n_hg, b = (int)(blockIdx.x / (unsigned)ub), r = (int)(blockIdx.x % (unsigned)ub);
   const int kvh = r / P.n_hg, hg = r % P.n_hg, nodes = clamp_nodes(p, b), rows = (int)P.group.d * p.n_q;
   constexpr int RW = (N + kWarpsQ - 1) / kWarpsQ;  // rows of a warp
+  if (__ldg(p.seq_lens + b) <= 0) {
+    for (int n = warp; n < N; n += kWarpsQ) {
+      const int vl = hg * N + n;
+      const long long row = vl < rows ? out_row(P, b, kvh, vl, nodes) : -1;
+      if (row < 0) continue;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+        *reinterpret_cast<uint2*>(static_cast<char*>(p.out) + ((size_t)row * D + blk * kBlock + 4 * lane) * 2) = make_uint2(0, 0);
+    }
+    return;
+  }
   float v[RW][NB][4];
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
