@@ -78,6 +78,9 @@ constexpr float kUnset = -1e30f;    // reference of a row that has seen no posit
 // 1, and the scale is chosen anew when one exceeds 2^9 (2^(6 + 9) fits fp16).
 constexpr int kNormTop = 7;
 constexpr float kNormRoom = 512.0f;
+// The scale before one is chosen: the smallest norm that is not zero exceeds it,
+// so the first tile that holds one chooses (until then the sum over V is zero).
+constexpr float kNoScale = 0x1p100f;
 constexpr uint32_t kPanel = 128 * 128;  // bytes of a 64-element x 128-row panel
 
 struct Plan {
@@ -714,7 +717,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
       float2 l[HC / 2];
 #pragma unroll
       for (int c = 0; c < HC / 2; ++c) l[c] = make_float2(0.0f, 0.0f);
-      float vpow = 1.0f;  // 2^-e of the V norms, e the unit's scale
+      float vpow = kNoScale;  // 2^-e of the V norms, e the segment's scale
       for (int tile = sg.lo; tile < sg.hi; ++tile, ++tile_no) {
         const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1;
         const int t = tile * kTok + tk, node = t - ctx;
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
               float vm = 0.0f;
 #pragma unroll
               for (int w = 0; w < 4; ++w) vm = fmaxf(vm, miscf[M::kVmax + 4 * grp + w]);
-              if (vm > 0.0f && (tile == sg.lo || vm * vpow > kNormRoom)) {
+              if (vm * vpow > kNormRoom) {
                 const float np = ldexpf(1.0f, kNormTop - ilogbf(vm));
                 beta = np / vpow;
                 vpow = np;

@@ -138,3 +138,24 @@ def test_empty_slots_cost_little():
         assert torch.all(out[:-1] == 0)
         return min(times[2:])
     assert best(64) <= 2 * best(1)
+
+
+@pytest.mark.parametrize("hq,dim", [(8, 128), (64, 128), (8, 256)])
+def test_small_v_norms_behind_zeros(hq, dim):
+    """The first 128 positions have V norms of zero and most of the weight, the
+    others 1 to 3 times the smallest norm that fp16 holds: they keep their
+    precision wherever a CTA's part starts.  Outputs are compared 2^24 times as large, so that the bound's
+    absolute term does not hide them."""
+    rng = np.random.default_rng(hq + dim)
+    B, hk, cap, n = 16, 8, 2048, 2
+    cache = R.random_cache(rng, B, hk, cap, dim, 3, 3)
+    cache[3][:] = (rng.integers(1, 4, cache[3].shape) * 2.0 ** -24).astype(np.float16)
+    cache[3][:, :, :128] = 0
+    cache[1][:, :, :128] *= 3
+    cache[2][:] = cache[2][:, :, :1]  # V of one direction: nothing cancels
+    lens = [cap] * B
+    assert _tiles(lens, hq, hk, n, dim, 16) > 12 * _sms()
+    masks, q = _trees(rng, B, n), rng.standard_normal((B, n, hq, dim))
+    got, q = _run(tq.kv_desc(B, hk, dim, cap, 3, 3), cache, hq, n, lens, [n] * B, masks, q, dst="bfloat16")
+    ref, spread, score = R.tree_attention(q, cache, 3, 3, lens, [n] * B, masks, dim ** -0.5)
+    R.check_tree(got * 2.0 ** 24, ref * 2.0 ** 24, spread * 2.0 ** 24, score, 2.0 ** -7)
