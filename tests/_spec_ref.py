@@ -97,6 +97,36 @@ def tree_attention(q, cache, k_bits, v_bits, lens, counts, masks, scale, seed=0)
     return out, spread, score
 
 
+def tree_attention_by_head(q, cache, k_bits, v_bits, lens, counts, masks, scale, seed=0):
+    """tree_attention, with the rows of one sequence and kv-head at a time."""
+    kc, kn, vc, vn = cache
+    s = O.sign_vector(seed)
+    B, n_q, hq, D = q.shape
+    hk = kc.shape[1]
+    g = hq // hk
+    out = np.full(q.shape, np.nan)
+    spread, score = np.zeros((B, n_q, hq, D // 128)), np.zeros((B, n_q, hq))
+    for b in range(B):
+        L, n = int(lens[b]), int(counts[b])
+        if n == 0:
+            continue
+        see = np.repeat(visible(L, n, masks[b]), g, axis=0)  # [n * g, L], node-major
+        for h in range(hk):
+            k, v = (O.dequantize(c[b, h, :L], m[b, h, :L], bits, O.codebook_f32(bits)[0].astype(np.float64), s)
+                    for c, m, bits in ((kc, kn, k_bits), (vc, vn, v_bits)))
+            qq = q[b, :n, h * g:(h + 1) * g].astype(np.float64).reshape(n * g, D)
+            x = np.where(see, scale * (qq @ k.T), -np.inf) if L else np.zeros((n * g, 0))
+            top = x.max(axis=1, initial=-np.inf, keepdims=True)
+            w = np.exp(x - np.where(top > -np.inf, top, 0.0))
+            w /= np.maximum(w.sum(axis=1, keepdims=True), 1e-300)
+            rows = (b, slice(0, n), slice(h * g, (h + 1) * g))
+            out[rows] = (w @ v).reshape(n, g, D)
+            spread[rows] = (w @ np.linalg.norm(v.reshape(L, D // 128, 128), axis=-1)).reshape(n, g, D // 128)
+            kmax = np.where(see, np.linalg.norm(k, axis=-1)[None], 0.0).max(axis=1, initial=0.0)
+            score[rows] = (scale * np.linalg.norm(qq, axis=-1) * kmax).reshape(n, g)
+    return out, spread, score
+
+
 def check_tree(got, ref, spread, score, eps_out):
     """Every 128-block of every row, in the 2-norm (the inverse rotation keeps
     it).  With u = 2^-11, half a step of fp16: a score x = scale q.k is off by at

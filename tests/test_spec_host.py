@@ -187,3 +187,15 @@ def test_binding_refuses_before_the_library():
 def test_binding_refuses_max_rows_that_its_int_cannot_hold():
     with pytest.raises(ValueError, match="max_rows"):
         tq.cache_copy(None, None, None, None, None, 2 ** 32)
+
+
+def test_the_two_plain_forms_of_tree_attention_agree():
+    rng = np.random.default_rng(0)
+    cache = R.random_cache(rng, 3, 2, 40, 256, 3, 2)
+    q = rng.standard_normal((3, 4, 6, 256))
+    masks = np.array([[1, 3, 0, 9], [1, 2, 5, 8], [0, 2, 4, 8]], dtype=np.int64)
+    args = (q, cache, 3, 2, [40, 4, 0], [4, 3, 2], masks, 0.0625, 5)
+    for x, y in zip(R.tree_attention(*args), R.tree_attention_by_head(*args)):
+        assert np.array_equal(np.isnan(x), np.isnan(y))
+        live = ~np.isnan(x)
+        assert np.allclose(x[live], y[live], rtol=1e-12, atol=1e-12)

@@ -63,7 +63,7 @@ def test_mostly_empty_batches():
     masks, q = _trees(rng, B, n), rng.standard_normal((B, n, hq, 128))
     got, q = _run(tq.kv_desc(B, hk, 128, cap, 3, 3), cache, hq, n, lens, counts, masks, q)
     at = list(live)
-    ref, spread, score = R.tree_attention(q[at], small, 3, 3, [lens[b] for b in at], [n] * 2, masks[at], 128 ** -0.5)
+    ref, spread, score = R.tree_attention_by_head(q[at], small, 3, 3, [lens[b] for b in at], [n] * 2, masks[at], 128 ** -0.5)
     R.check_tree(got[at], ref, spread, score, 2.0 ** -10)
     for b in range(B):
         if b not in live:
@@ -94,8 +94,8 @@ for hq, hk, dim in ((8, 4, 128), (32, 2, 256), (64, 4, 128)):
     multi = torch.zeros(q.shape, device="cuda")
     tq.decode_attention_multi(cache, cb, cb, q, lens, dim ** -0.5, multi, tq.alloc_workspace(desc, hq * n))
     chain = np.stack([tq.tree_masks([-1, 0, 1, 2, 3, 4])[0]] * 4)
-    ref, spread, score = R.tree_attention(q[:, :1].double().cpu().numpy(), (kc, kn, vc, vn), 3, 3,
-                                          (lens - n + 1).tolist(), [1] * 4, chain[:, :1], dim ** -0.5)
+    ref, spread, score = R.tree_attention_by_head(q[:, :1].double().cpu().numpy(), (kc, kn, vc, vn), 3, 3,
+                                                  (lens - n + 1).tolist(), [1] * 4, chain[:, :1], dim ** -0.5)
     R.check_tree(multi[:, :1].double().cpu().numpy(), ref, spread, score, 2.0 ** -23)
 assert states <= {0, TQ_DEV_INTERNAL}, states
 print("states", sorted(states))
@@ -157,5 +157,59 @@ def test_small_v_norms_behind_zeros(hq, dim):
     assert _tiles(lens, hq, hk, n, dim, 16) > 12 * _sms()
     masks, q = _trees(rng, B, n), rng.standard_normal((B, n, hq, dim))
     got, q = _run(tq.kv_desc(B, hk, dim, cap, 3, 3), cache, hq, n, lens, [n] * B, masks, q, dst="bfloat16")
-    ref, spread, score = R.tree_attention(q, cache, 3, 3, lens, [n] * B, masks, dim ** -0.5)
+    ref, spread, score = R.tree_attention_by_head(q, cache, 3, 3, lens, [n] * B, masks, dim ** -0.5)
     R.check_tree(got * 2.0 ** 24, ref * 2.0 ** 24, spread * 2.0 ** 24, score, 2.0 ** -7)
+
+
+# rows of a kv-head: the columns of their row group (16 to 128, or 64 for heads of 256) and 104 to 200 rows in two
+ROWS = [(128, 1, 9, 16), (128, 4, 7, 32), (128, 8, 7, 64), (128, 8, 13, 128), (128, 8, 25, 128),
+        (256, 1, 9, 16), (256, 4, 7, 32), (256, 8, 7, 64), (256, 4, 25, 64)]
+
+
+@pytest.mark.parametrize("norms", ["even", "growing", "falling", "mixed"])
+@pytest.mark.parametrize("dim,group,n,columns", ROWS)
+def test_parts_of_many_tiles(dim, group, n, columns, norms):
+    """More than four tiles in every CTA, sequences of uneven lengths and trees.
+    Growing K norms let late scores exceed early ones by far more than 2^6, so the
+    references move and the sums are rescaled inside a part; growing V norms move
+    their scale; falling ones leave both; mixed ones change from tile to tile."""
+    rng = np.random.default_rng(dim + 8 * n + group)
+    hk = 4
+    units = 4 * hk * (2 if group * n > columns else 1)  # of four sequences
+    B, cap = 4, 2 * (4 * _sms() * 128 // units // 2) + 600
+    lens = [cap, cap - 129, cap - 511, cap - 300]
+    counts = [n, n - 1, max(1, n // 2), n]
+    kb, vb = {"even": (3, 3), "growing": (4, 2), "falling": (2, 4), "mixed": (3, 2)}[norms]
+    cache = R.random_cache(rng, B, hk, cap, dim, kb, vb)
+    ramp = np.linspace(0, 1, cap)[None, None, :, None]
+    if norms == "mixed":
+        ramp = np.repeat(rng.random((B, hk, -(-cap // 128), 1)), 128, axis=2)[:, :, :cap]
+    if norms != "even":
+        t = 1 - ramp if norms == "falling" else ramp
+        cache[1] = (cache[1].astype(np.float64) * (0.1 + 3.9 * t)).astype(np.float16)
+        cache[3] = (cache[3].astype(np.float64) * 10 ** (-4 + 7 * t)).astype(np.float16)
+    hq = group * hk
+    assert _tiles(lens, hq, hk, n, dim, columns) > 4 * _sms()
+    masks, q = _trees(rng, B, n), rng.standard_normal((B, n, hq, dim))
+    got, q = _run(tq.kv_desc(B, hk, dim, cap, kb, vb), cache, hq, n, lens, counts, masks, q, dst="bfloat16")
+    ref, spread, score = R.tree_attention_by_head(q, cache, kb, vb, lens, counts, masks, dim ** -0.5)
+    assert np.all(got[np.isnan(ref)] == 3.0)
+    R.check_tree(got, ref, spread, score, 2.0 ** -7)
+
+
+@pytest.mark.parametrize("v_levels", [1.0, 1.25])
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("dim,group,n,columns", [(128, 8, 13, 128), (256, 8, 13, 64)])
+def test_parts_of_many_tiles_with_the_fullest_shared_memory(dim, group, n, columns, bits, v_levels):
+    """104 rows, K and V of one width: one code table for both or two (the V sum is
+    linear in its levels), fewer stages and slots the fuller the memory."""
+    rng = np.random.default_rng(dim + bits)
+    B, hk, cap = 2, 4, 2 * (4 * _sms() * 128 // 16) + 400
+    lens = [cap, cap - 200]
+    cache = R.random_cache(rng, B, hk, cap, dim, bits, bits)
+    hq = group * hk
+    assert _tiles(lens, hq, hk, n, dim, 128) > 2 * _sms()
+    masks, q = _trees(rng, B, n), rng.standard_normal((B, n, hq, dim))
+    got, q = _run(tq.kv_desc(B, hk, dim, cap, bits, bits), cache, hq, n, lens, [n] * B, masks, q, v_levels=v_levels)
+    ref, spread, score = R.tree_attention_by_head(q, cache, bits, bits, lens, [n] * B, masks, dim ** -0.5)
+    R.check_tree(got, ref, spread, score, 2.0 ** -10)
