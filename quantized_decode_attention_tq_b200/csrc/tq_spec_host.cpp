@@ -43,7 +43,7 @@ tq::CacheView view(const tq_kv_desc* d, const tq_cache_bufs* c) {
                        d->seq_cap};
 }
 
-int check_rows(const tq_rows* r, int dtype, int w_dtype, int head_dim, bool weighted, tq::RowSide* out) {
+int check_rows(const tq_rows* r, int dtype, int w_dtype, bool weighted, tq::RowSide* out) {
   *out = tq::RowSide{};
   if (!r) return TQ_OK;
   if (r->heads < 1 || !r->in || !r->out || !aligned(r->in, 16) || !aligned(r->out, 16)) return TQ_ERR_INVALID_ARG;
@@ -59,7 +59,6 @@ int check_rows(const tq_rows* r, int dtype, int w_dtype, int head_dim, bool weig
   out->batch_stride = r->batch_stride;
   out->token_stride = r->token_stride;
   out->head_stride = r->head_stride;
-  (void)head_dim;
   return TQ_OK;
 }
 
@@ -116,19 +115,19 @@ int tq_qk_norm_rope(const tq_rope* rope, int batch, int seq_new, int head_dim, c
     if (rope->rot_dim < 0 || rope->rot_dim % 2 != 0 || rope->rot_dim > head_dim || !std::isfinite(rope->gain))
       return TQ_ERR_INVALID_ARG;
   }
+  if (norm && (!std::isfinite(eps) || !(eps >= 0.0f) || !std::isfinite(weight_bias))) return TQ_ERR_INVALID_ARG;
+  if (seq_new == 0) return TQ_OK;  // empty tensors need not have addresses
   const bool rotates = rope && rope->rot_dim > 0 && (q || k);
   if (rotates && !positions) return TQ_ERR_INVALID_ARG;
-  if (norm && (!std::isfinite(eps) || !(eps >= 0.0f) || !std::isfinite(weight_bias))) return TQ_ERR_INVALID_ARG;
   if (!aligned(positions, 4) || !aligned(n_tok, 4)) return TQ_ERR_INVALID_ARG;
   tq::RopeParams p{};
   const tq_rows* sides[3] = {q, k, v};
   for (int s = 0; s < 3; ++s) {
-    const int st = check_rows(sides[s], in_dtype, w_dtype, head_dim, norm && s < 2, &p.side[s]);
+    const int st = check_rows(sides[s], in_dtype, w_dtype, norm && s < 2, &p.side[s]);
     if (st != TQ_OK) return st;
   }
   const long long rows = (long long)p.side[0].heads + p.side[1].heads + p.side[2].heads;
   if (rows > (1 << 20) || (long long)batch * seq_new >= (1LL << 31)) return TQ_ERR_UNSUPPORTED;
-  if (seq_new == 0) return TQ_OK;
   p.batch = batch;
   p.seq_new = seq_new;
   p.head_dim = head_dim;

@@ -625,3 +625,10 @@ def test_calls_follow_a_side_stream():
     tq.cache_copy(c, c, a, b, n, 64, stream=s)
     s.synchronize()
     assert torch.all(c.k_codes[1] == 4)
+
+
+def test_rope_of_no_tokens():
+    torch = torch_mod()
+    q, k = (torch.empty(2, 0, h, 128, device="cuda", dtype=torch.float16) for h in (4, 2))
+    tq.qk_norm_rope(tq.make_rope(64), q, k, k, torch.empty(2, 0, device="cuda", dtype=torch.int32), torch.empty_like(q),
+                    k.transpose(1, 2).contiguous(), k.transpose(1, 2).contiguous())

@@ -199,3 +199,13 @@ def test_the_two_plain_forms_of_tree_attention_agree():
         assert np.array_equal(np.isnan(x), np.isnan(y))
         live = ~np.isnan(x)
         assert np.allclose(x[live], y[live], rtol=1e-12, atol=1e-12)
+
+
+def test_norm_rope_of_no_tokens_is_a_no_op_without_addresses():
+    """Empty tensors have a null address."""
+    f, rows = tq.lib().tq_qk_norm_rope, _lib.Rows(None, None, None, 4, 0, 0, 0)
+    rope = tq.make_rope(64)
+    args = [ctypes.byref(rope), 2, 0, 128, ctypes.byref(rows), None, None, 1, 1, 1, 1, 1e-6, 0.0, None, None, None]
+    assert f(*args) == OK
+    assert f(*args[:3], 96, *args[4:]) == UNS and f(*args[:7], 3, *args[8:]) == BAD  # the rest is still checked
+    assert f(*args[:2], 1, *args[3:]) == BAD
