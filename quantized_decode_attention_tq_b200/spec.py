@@ -244,8 +244,8 @@ def cache_copy(src: Cache, dst: Cache, src_slot, dst_slot, n_rows, max_rows: int
                src_vo: VOutliers | None = None, dst_vo: VOutliers | None = None, status=None, stream=None) -> None:
     """Copy row ranges between cache slots (tq_cache_copy): n_rows[c] rows from
     src_pos[c] of slot src_slot[c] to dst_pos[c] of slot dst_slot[c]."""
-    if max_rows >= 2 ** 31:  # would lose its upper bits on the way
-        raise ValueError("max_rows must be below 2^31")
+    if not 0 <= max_rows < 2 ** 31:  # others would lose their upper bits on the way
+        raise ValueError("max_rows must be in [0, 2^31)")
     dev = _device(src.k_codes, "k_codes")
     n = src_slot.shape[0]
     shape = (n,)

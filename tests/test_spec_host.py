@@ -209,3 +209,9 @@ def test_norm_rope_of_no_tokens_is_a_no_op_without_addresses():
     assert f(*args) == OK
     assert f(*args[:3], 96, *args[4:]) == UNS and f(*args[:7], 3, *args[8:]) == BAD  # the rest is still checked
     assert f(*args[:2], 1, *args[3:]) == BAD
+
+
+def test_binding_refuses_max_rows_below_zero():
+    for n in (-1, -2 ** 32 + 5):  # the second's lower bits are 5
+        with pytest.raises(ValueError, match="max_rows"):
+            tq.cache_copy(None, None, None, None, None, n)
