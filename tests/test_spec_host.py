@@ -215,3 +215,13 @@ def test_binding_refuses_max_rows_below_zero():
     for n in (-1, -2 ** 32 + 5):  # the second's lower bits are 5
         with pytest.raises(ValueError, match="max_rows"):
             tq.cache_copy(None, None, None, None, None, n)
+
+
+def test_packed_structures_are_the_declared_ones():
+    """The binding packs tq_rows and tq_cache_bufs; their fields lie where the structures have them."""
+    from quantized_decode_attention_tq_b200 import spec
+    rows = _lib.Rows.from_buffer_copy(spec._ROWS.pack(1, 2, 3, 4, 5, 6, 7))
+    assert [getattr(rows, n) for n, _ in _lib.Rows._fields_] == [1, 2, 3, 4, 5, 6, 7]
+    bufs = _lib.CacheBufs.from_buffer_copy(spec._BUFS.pack(1, 2, 3, 4, 5, 6))
+    assert [getattr(bufs, n) for n, _ in _lib.CacheBufs._fields_] == [1, 2, 3, 4, 5, 6]
+    assert spec._ROWS.size == ctypes.sizeof(_lib.Rows) and spec._BUFS.size == ctypes.sizeof(_lib.CacheBufs)
