@@ -28,8 +28,9 @@
  *     programmatic stream serialisation, so a decode launch may start while
  *     the kernel before it in the stream is still running if that kernel
  *     signals its dependents early (griddepcontrol.launch_dependents /
- *     cudaTriggerProgrammaticLaunchCompletion; of this library's kernels only
- *     the decode kernel does).  The launch reads `seq_lens` before it waits
+ *     cudaTriggerProgrammaticLaunchCompletion; of this library's kernels the
+ *     decode kernel does, and that of tq_decode_attention_tree, which writes
+ *     no seq_lens, where no join follows it).  The launch reads `seq_lens` before it waits
  *     for that kernel and everything else (query, cache, new rows, workspace,
  *     output) after: a preceding kernel that signals early must not write
  *     `seq_lens` after its signal.  After any other kernel, a copy or an

@@ -134,6 +134,11 @@ size_t tq_tree_workspace_size(const tq_kv_desc* desc, int q_heads, int n_q);
  *     cache's start do not exist: no row sees them.
  *   - Values in positions that a row does not see (infinite or NaN norms
  *     included) do not reach it.
+ *   - Range: the rows of a kv-head are worked on in groups of up to 128, whose
+ *     queries share one power-of-two scale; a row whose largest finite |q| is
+ *     below 2^-20 of its group's keeps less of q than fp16 would.  V norms share
+ *     a scale along the sequence: one below 2^-21 of the largest (of any cached
+ *     position, seen or not) is rounded coarser than fp16 at a weight of 1.
  *   - workspace: tq_tree_workspace_size() bytes, 256-byte aligned, any
  *     content; calls that share one must not overlap in time.  Three launches
  *     (queries, attention, join), the last two as programmatic dependents.

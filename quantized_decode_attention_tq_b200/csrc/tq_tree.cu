@@ -7,7 +7,7 @@
 // Mapping.  A unit is a (sequence, kv-head, group of up to N query rows); the
 // rows of a kv-head (nodes x heads of the group) share its K and V.  All
 // 128-position tiles of all units are laid end to end and cut evenly over one
-// persistent CTA per SM.  Per tile, codes become fp16 once for all N rows:
+// persistent CTA per SM (tq_tree_cut.h).  Per tile, codes become fp16 once for all N rows:
 //   S^T [128 positions x N rows] = K^ [128 x D] . Q^T     (tcgen05, M = 128)
 //   O^T [128 dims x N rows]     += V^T [128 x 128] . P    per 128-block
 // Positions are the MMA's rows, so N adapts to the tree (16 to 128 columns), a
@@ -24,14 +24,17 @@
 //
 // Roundings to fp16, all others are fp32: the query is split in two fp16 terms
 // (two MMAs), the centroids are scaled by a factor that makes their rounding
-// small (centroid_scale), and weight * norm is rounded once.
+// small (centroid_scale), and weight * norm is rounded once.  A row group's
+// queries share one power-of-two scale (a scale per row would cost the softmax a
+// product per score), and a part's V norms another.
 //
-// What it measured (a pass, one B200): trees of 16 nodes on 8 x 32768 positions
-// of 3 + 3 bits 166 us, 64 nodes on 131072 of 4 + 2 bits 272 us.  A tile of 64
-// columns takes about 2500 cycles and 6500 warp instructions (1300 for K, 930
-// for V, 3600 in the softmax) with 58% of the issue slots, 61% of the
-// shared-memory bandwidth and 24% of the tensor pipe taken: no unit is full,
-// the latencies of its 28 warps bind.
+// What it measured (on the device, one B200; a pass through the binding takes
+// some 6 us more): trees of 16 nodes on 8 x 32768 positions of 3 + 3 bits
+// 166 us, 64 nodes on 131072 of 4 + 2 bits 269 us.  A tile of 64 columns takes
+// about 2500 cycles and 6500 warp instructions (1300 for K, 930 for V, 3600 in
+// the softmax) with 57% of the issue slots, 60% of the shared-memory bandwidth
+// and 24% of the tensor pipe taken: no unit is full, the latencies of its 28
+// warps bind.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,8 +59,9 @@ constexpr int kTok = 128;  // positions per tile
 // one for V; one whose warps issue the score MMAs, the V MMAs and the copies.
 // Four softmax groups from 64 columns on: with two, 64 columns took 198 us
 // where four take 188 (8 x 32768 positions).  Registers per thread at launch,
-// then by role; the shares must fit the launch's total.  At four groups 80, 64
-// and 56 leave 64 columns without spills (other splits: 3 to 25% slower).
+// then by role; the shares must fit the launch's total.  Other splits were 3 to
+// 25% slower.  With this one a thread spills up to 8 bytes in heads of one block
+// at 16 to 64 columns, 52 at 128, and 72 to 216 in heads of two.
 template <int N>
 struct Roles {
   static constexpr int kGroups = N >= 64 ? 4 : 2;
@@ -1048,7 +1052,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) tree_kernel(const __gri
     else by_bits(p.k_bits, std::false_type{});
   } else {
     // ================================================================= MMAs
-    // Warp 16 issues the score products, warp 17 the V sums.  Descriptors and
+    // The first warp issues the score products, the second the V sums, the
+    // third the copies of the codes, the fourth those of Q^.  Descriptors and
     // loop bounds are warp-uniform, so that they stay in uniform registers: an
     // MMA of these shapes takes 32 to 64 cycles, and moving its descriptors
     // into place must not take longer.
