@@ -213,3 +213,45 @@ def test_parts_of_many_tiles_with_the_fullest_shared_memory(dim, group, n, colum
     got, q = _run(tq.kv_desc(B, hk, dim, cap, bits, bits), cache, hq, n, lens, [n] * B, masks, q, v_levels=v_levels)
     ref, spread, score = R.tree_attention_by_head(q, cache, bits, bits, lens, [n] * B, masks, dim ** -0.5)
     R.check_tree(got, ref, spread, score, 2.0 ** -10)
+
+
+def test_a_captured_call_follows_slots_that_come_and_go():
+    """One graph, replayed with other lengths and node counts in the same tensors:
+    all slots empty, one live, short ones, long ones (cuts with and without ends)."""
+    torch = torch_mod()
+    rng = np.random.default_rng(3)
+    B, hk, hq, cap, n = 24, 8, 16, 4000, 3
+    cache = R.random_cache(rng, B, hk, cap, 128, 2, 3)
+    desc = tq.kv_desc(B, hk, 128, cap, 2, 3)
+    dc = tq.Cache(desc, *(to_dev(x if x.dtype == np.uint8 else x.view(np.int16)) for x in cache))
+    k_cb, v_cb = tq.make_codebook(2), tq.make_codebook(3)
+    q = torch.randn(B, n, hq, 128, device="cuda", dtype=torch.float16)
+    masks = to_dev(_trees(rng, B, n))
+    lens, counts = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    out, eager, ws = torch.zeros_like(q), torch.zeros_like(q), tq.alloc_tree_workspace(desc, hq, n)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(o):
+        tq.decode_attention_tree(dc, k_cb, v_cb, q, lens, masks, 0.0884, o, ws, n_nodes=counts, status=status)
+    call(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    long = rng.integers(3000, cap + 1, B)
+    for live in (np.zeros(B, dtype=int), np.where(np.arange(B) == 13, cap, 0), rng.integers(0, 300, B),
+                 long * (rng.random(B) < 0.5), long, np.zeros(B, dtype=int)):
+        lens.copy_(torch.from_numpy(live))
+        counts.copy_(torch.from_numpy(rng.integers(0, n + 1, B)))
+        out.fill_(3.0), eager.fill_(3.0)
+        graph.replay()
+        call(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+        nodes = counts.tolist()
+        ref, spread, score = R.tree_attention_by_head(q.double().cpu().numpy(), cache, 2, 3, live, nodes,
+                                                      masks.cpu().numpy(), 0.0884)
+        got = out.double().cpu().numpy()
+        assert np.all(got[np.isnan(ref)] == 3.0)
+        R.check_tree(got, ref, spread, score, 2.0 ** -10)
+    assert tq.read_device_status(status) == 0
